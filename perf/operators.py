@@ -25,7 +25,7 @@ own = False
 
 DEV = "cuda"
 F32, BF16 = torch.float32, torch.bfloat16
-EPS = 1e-5
+EPS = 9.999999747378752e-06  # 1e-5 in fp32
 
 
 def _dt(name):
