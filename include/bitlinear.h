@@ -440,6 +440,105 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
                              float* dW, void* workspace, size_t ws_bytes, bl_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * 4-bit weights with group scales, for the matrices of a model that are not
+ * ternarised (the language-model head, the first and last projections). The
+ * pages have no counterpart.
+ *   w[n, k] = s[n, k/group] · (q[n, k] − z[n, k/group]),  q in 0..15,
+ *   group 32, 64 or 128 columns (the last one of a row may be short),
+ *   s bf16; z = 8 (zeros NULL: symmetric) or a stored byte 0..15.
+ * Layout: blocks of 16 rows × 128 columns, 1024 bytes each, the blocks of a
+ * row block one after the other (ceil(N/16) × ceil(K/128) of them). Word
+ * (h, g, t, u), u fastest, of a block (h 0..1, g 0..7, t 0..3, u 0..3) holds
+ * row 16·rb + 8·h + g, columns 128·kb + 32·u + 8·t + (0..7), column 2·p + e of
+ * those at bit 4·p + 16·e. Scales (and zero points) are [rb][kb][g][128/group]
+ * [h]: bl_w4_scale_count() of them. What lies past row N or column K has
+ * scale 0 and is never part of a result.
+ *   bl_quant_weights_w4  W [N, K] fp32/bf16 → W4 (bl_w4_bytes() bytes), scales
+ *     and, when zeros is not NULL, zero points. Symmetric: s = bf16(max|w|/7),
+ *     q = 8 + Round(w/s). With zero points: lo = min(w, 0), hi = max(w, 0),
+ *     s = bf16((hi − lo)/15), z = Clip(Round(−lo/s), 0, 15),
+ *     q = Clip(Round(w/s) + z, 0, 15). The quotients are rounded as the exact
+ *     ones, ties to even; s is an fp32 quotient rounded to bf16. A group whose
+ *     s is 0 holds zeros.
+ *   bl_pack_w4    codes found elsewhere: codes [N, K/2] (the lower column in the
+ *     low half of a byte), scales [N, ceil(K/group)] bf16, zero points of the
+ *     same shape (or both NULL) → the layout above.
+ *   bl_unpack_w4  the matrix [N, K] the packed weights stand for (exact in fp32;
+ *     one rounding for bf16).
+ *   bl_linear_w4  Y [M, N] = X·Wᵀ from fp32/bf16 activations [M, K], for few
+ *     tokens (any M is taken; the weights are read again for every group of
+ *     tokens a launch takes at once). Products are exact and
+ *     the sums are fp32 (an fp32 X is split into three bf16 pieces whose sum it
+ *     is). flags: BL_FLAG_PDL as for bl_linear_ex. */
+size_t bl_w4_bytes(int64_t N, int64_t K);
+int64_t bl_w4_scale_count(int64_t N, int64_t K, int group);
+bl_status bl_quant_weights_w4(const void* W, bl_dtype w_dtype, int64_t N, int64_t K, int group,
+                              uint8_t* W4, void* scales, uint8_t* zeros, bl_stream_t stream);
+bl_status bl_pack_w4(const uint8_t* codes, const void* scales_in, const uint8_t* zeros_in,
+                     int64_t N, int64_t K, int group, uint8_t* W4, void* scales, uint8_t* zeros,
+                     bl_stream_t stream);
+bl_status bl_unpack_w4(const uint8_t* W4, const void* scales, const uint8_t* zeros, int64_t N,
+                       int64_t K, int group, void* W, bl_dtype w_dtype, bl_stream_t stream);
+bl_status bl_linear_w4(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, const uint8_t* W4,
+                       const void* scales, const uint8_t* zeros, int64_t N, int group, void* Y,
+                       bl_dtype y_dtype, unsigned flags, bl_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Layer norm in front of the activation quantiser, and its backward. The pages
+ * put no norm inside BitLinear; a model that has one in front of it runs it
+ * here, to floats or straight to the int8 tokens of bl_linear_q.
+ *   mean = Σx/K, d = x − mean, rstd = 1/sqrt(Σd²/K + eps) (the two sums in 64
+ *   bits, mean and rstd rounded once to fp32), x̂ = d·rstd, y = x̂·weight + bias
+ *   (fp32, one operation each, in this order; bias NULL: none).
+ *   bl_layernorm        Y [M, K] = y as fp32/bf16; mean, rstd [M] (NULL: not kept).
+ *   bl_layernorm_quant  the tokens that bl_quant_acts makes of y (q_eps is its
+ *     eps; rowsum may be NULL), without y going through memory; rstd [M] (NULL:
+ *     not kept) and, when xhat_q is not NULL, an 8-bit checkpoint of x̂
+ *     (xhat_q [M, K] int8, xhat_scale [M, K/64]) for bl_layernorm_grad_q8.
+ *   bl_layernorm_grad   from dY [M, K] and the kept X, mean and rstd:
+ *     g = weight·dY, dX = rstd·(g − mean(g) − x̂·mean(g·x̂)) as fp32/bf16,
+ *     dweight [K] = Σ_m dY·x̂, dbias [K] = Σ_m dY (NULL: not wanted). Column
+ *     sums are taken in a fixed order. M = 0 writes zeros.
+ *   bl_layernorm_grad_q8  the same from the 8-bit checkpoint of x̂; neither X nor
+ *     mean is needed.
+ * 8-bit checkpoints: groups of 64 columns with one fp32 scale; m = max|v| of a
+ * group, codes Round(v·(127/m)), scale m/127 (unsigned: 255); a group with
+ * m < 2^-100 holds zeros. An element is off by at most half a step (plus fp32
+ * rounding). Inputs and outputs must not overlap. weight and bias are fp32. */
+bl_status bl_layernorm(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, const float* weight,
+                       const float* bias, float eps, void* Y, bl_dtype y_dtype, float* mean,
+                       float* rstd, bl_stream_t stream);
+bl_status bl_layernorm_quant(const void* X, bl_dtype x_dtype, int64_t M, int64_t K,
+                             const float* weight, const float* bias, float eps, float q_eps,
+                             int8_t* A_q, float* gamma_A, int32_t* rowsum, float* rstd,
+                             int8_t* xhat_q, float* xhat_scale, bl_stream_t stream);
+size_t bl_layernorm_grad_workspace_bytes(int64_t M, int64_t K);
+bl_status bl_layernorm_grad(const void* dY, bl_dtype dy_dtype, const void* X, bl_dtype x_dtype,
+                            const float* mean, const float* rstd, const float* weight, int64_t M,
+                            int64_t K, void* dX, bl_dtype dx_dtype, float* dweight, float* dbias,
+                            void* workspace, size_t ws_bytes, bl_stream_t stream);
+bl_status bl_layernorm_grad_q8(const void* dY, bl_dtype dy_dtype, const int8_t* xhat_q,
+                               const float* xhat_scale, const float* rstd, const float* weight,
+                               int64_t M, int64_t K, void* dX, bl_dtype dx_dtype, float* dweight,
+                               float* dbias, void* workspace, size_t ws_bytes, bl_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * ReLU² of the FFN block in training, with an 8-bit checkpoint of its input.
+ *   bl_relu2_requant_q8  from the up-projection's INT32 accumulators [M, H]:
+ *     h = acc·((gamma_x·gamma_up)/127), p = max(h, 0), r = p² (fp32); the tokens
+ *     R_q [M, H], gamma_r [M] and rowsum [M] (may be NULL) of the down-projection,
+ *     as in bl_ffn_relu2, and the unsigned checkpoint of p (P_q [M, H] bytes,
+ *     p_scale [M, H/64]).
+ *   bl_relu2_grad_q8     dH [M, H] = 2·p̂·dR, p̂ = p_scale·P_q; dR fp32/bf16, dH
+ *     fp32/bf16 (bf16 is what bl_ste_grad_weight / _input take without a copy). */
+bl_status bl_relu2_requant_q8(const int32_t* acc_up, const float* gamma_x, const float* gamma_up,
+                              int64_t M, int64_t H, float eps, int8_t* R_q, float* gamma_r,
+                              int32_t* rowsum, uint8_t* P_q, float* p_scale, bl_stream_t stream);
+bl_status bl_relu2_grad_q8(const void* dR, bl_dtype dr_dtype, const uint8_t* P_q,
+                           const float* p_scale, int64_t M, int64_t H, void* dH, bl_dtype dh_dtype,
+                           bl_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Device error flag. Synchronises `stream`, then returns BL_ERR_TIMEOUT if
  * any kernel of this library on the current device gave up a bounded wait
  * since the last check (and clears the flag), BL_ERR_CUDA if the stream

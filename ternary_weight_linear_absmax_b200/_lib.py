@@ -82,6 +82,23 @@ SIGNATURES = {
     "bl_ste_grad_weight_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "bl_ste_grad_weight": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _i64, _vp, _int, _vp, _f32,
                                   _vp, _vp, _sz, _vp]),
+    "bl_w4_bytes": (_sz, [_i64, _i64]),
+    "bl_w4_scale_count": (_i64, [_i64, _i64, _int]),
+    "bl_quant_weights_w4": (_int, [_vp, _int, _i64, _i64, _int, _vp, _vp, _vp, _vp]),
+    "bl_pack_w4": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _vp]),
+    "bl_unpack_w4": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _vp, _int, _vp]),
+    "bl_linear_w4": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _i64, _int, _vp, _int, _uint,
+                            _vp]),
+    "bl_layernorm": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _f32, _vp, _int, _vp, _vp, _vp]),
+    "bl_layernorm_quant": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _f32, _f32, _vp, _vp, _vp, _vp,
+                                  _vp, _vp, _vp]),
+    "bl_layernorm_grad_workspace_bytes": (_sz, [_i64, _i64]),
+    "bl_layernorm_grad": (_int, [_vp, _int, _vp, _int, _vp, _vp, _vp, _i64, _i64, _vp, _int, _vp,
+                                 _vp, _vp, _sz, _vp]),
+    "bl_layernorm_grad_q8": (_int, [_vp, _int, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _int, _vp, _vp,
+                                    _vp, _sz, _vp]),
+    "bl_relu2_requant_q8": (_int, [_vp, _vp, _vp, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "bl_relu2_grad_q8": (_int, [_vp, _int, _vp, _vp, _i64, _i64, _vp, _int, _vp]),
     "bl_probe_pdl_floor": (_int, [_i64, _i64, _i64, _vp]),
     "bl_check_device_error": (_int, [_vp]),
     "bl_selftest_wait_timeout": (_int, [_i64, _vp]),

@@ -13,10 +13,12 @@
 #include "gemv_kernel.cuh"
 #include "gemv_lut_kernel.cuh"
 #include "gemv_r3_kernel.cuh"
+#include "norm_kernels.cuh"
 #include "quant_kernels.cuh"
 #include "skinny_kernel.cuh"
 #include "ste_kernels.cuh"
 #include "tc_gemm_kernel.cuh"
+#include "w4_kernels.cuh"
 
 namespace bl {
 namespace {
@@ -839,6 +841,126 @@ bl_status run_bf16_gemm(const void* A, int64_t lda, const void* B, int64_t ldb, 
   const bool dual = wide && tiles > dev_sms;
   return mask ? launch_gemm_form<kMajAMN | kMajBMN, true>(ta, tb, p, wide, dual, dev, st)
               : launch_gemm_form<kMajBMN, false>(ta, tb, p, wide, dual, dev, st);
+}
+
+// --------------------------------------------------------------------------
+// 4-bit weights.
+bl_status check_group(int group) {
+  return group == 32 || group == 64 || group == 128 ? BL_OK : BL_ERR_SHAPE;
+}
+inline size_t w4_blocks(int64_t N, int64_t K) {
+  return (size_t)((N + 15) / 16) * (size_t)((K + 127) / 128);
+}
+// Grid of a loop over `items` work items, `per` to a CTA.
+inline unsigned loop_grid(int64_t items, int64_t per, int sms) {
+  int64_t b = (items + per - 1) / per;
+  if (b > 16 * (int64_t)sms) b = 16 * (int64_t)sms;
+  return (unsigned)(b < 1 ? 1 : b);
+}
+
+template <typename T>
+bl_status launch_w4(const W4Params& p, int group, cudaStream_t st) {
+  const int64_t tok = sizeof(T) == 2 ? 8 : 2;
+  const int64_t gy = (p.M + tok - 1) / tok;
+  const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)(gy < 65535 ? gy : 65535));
+  if (group == 32)
+    w4_linear_kernel<T, 32><<<grid, kW4Threads, 0, st>>>(p);
+  else if (group == 64)
+    w4_linear_kernel<T, 64><<<grid, kW4Threads, 0, st>>>(p);
+  else
+    w4_linear_kernel<T, 128><<<grid, kW4Threads, 0, st>>>(p);
+  BL_CUDA(cudaGetLastError());
+  return BL_OK;
+}
+
+// --------------------------------------------------------------------------
+// Layer norm and 8-bit checkpoints.
+template <typename T>
+bl_status launch_norm(const NormParams& p, int out, cudaStream_t st) {
+  const dim3 grid((unsigned)p.M);
+  if (out == 0)
+    layernorm_kernel<T, float><<<grid, kNormThreads, 0, st>>>(p);
+  else if (out == 1)
+    layernorm_kernel<T, __nv_bfloat16><<<grid, kNormThreads, 0, st>>>(p);
+  else
+    layernorm_kernel<T, int8_t><<<grid, kNormThreads, 0, st>>>(p);
+  BL_CUDA(cudaGetLastError());
+  return BL_OK;
+}
+
+inline int64_t norm_grad_parts(int64_t M) { return M < kNormGradParts ? M : kNormGradParts; }
+
+template <typename TD, typename TX>
+bl_status launch_norm_grad(const NormGradParams& p, bl_dtype dx_dtype, int grid, cudaStream_t st) {
+  if (dx_dtype == BL_BF16)
+    layernorm_grad_kernel<TD, TX, __nv_bfloat16><<<grid, kNormThreads, 0, st>>>(p);
+  else
+    layernorm_grad_kernel<TD, TX, float><<<grid, kNormThreads, 0, st>>>(p);
+  BL_CUDA(cudaGetLastError());
+  return BL_OK;
+}
+
+// The two forms of the backward: from the input (x_dtype fp32/bf16) or from
+// the 8-bit checkpoint of x̂ (x_dtype < 0).
+bl_status norm_grad_impl(const void* dY, bl_dtype dy_dtype, const void* X, int x_dtype,
+                         const float* xs, const float* mean, const float* rstd,
+                         const float* weight, int64_t M, int64_t K, void* dX, bl_dtype dx_dtype,
+                         float* dweight, float* dbias, void* workspace, size_t ws_bytes,
+                         bl_stream_t stream) {
+  BL_TRY(check_dtype(dy_dtype));
+  BL_TRY(check_dtype(dx_dtype));
+  if (x_dtype >= 0) BL_TRY(check_dtype(x_dtype));
+  BL_TRY(check_k(K));
+  BL_TRY(check_rows(M));
+  BL_TRY(check_ptr(dweight));
+  if (dbias != nullptr) BL_TRY(check_ptr(dbias));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    int dev, sms;
+    BL_TRY(current_device(&dev, &sms));
+    BL_CUDA(cudaMemsetAsync(dweight, 0, (size_t)K * 4, st));
+    if (dbias != nullptr) BL_CUDA(cudaMemsetAsync(dbias, 0, (size_t)K * 4, st));
+    return BL_OK;
+  }
+  BL_TRY(check_ptr(dY));
+  BL_TRY(check_ptr(X));
+  if (x_dtype < 0)
+    BL_TRY(check_ptr(xs));
+  else
+    BL_TRY(check_ptr(mean));
+  BL_TRY(check_ptr(rstd));
+  BL_TRY(check_ptr(weight));
+  BL_TRY(check_ptr(dX));
+  if (workspace == nullptr || ws_bytes < bl_layernorm_grad_workspace_bytes(M, K))
+    return BL_ERR_WORKSPACE;
+  BL_TRY(check_ptr(workspace));
+  int dev, sms;
+  BL_TRY(current_device(&dev, &sms));
+  NormGradParams p = {};
+  p.dY = dY;
+  p.X = X;
+  p.xs = xs;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.weight = weight;
+  p.M = M;
+  p.K = K;
+  p.dX = dX;
+  p.part = reinterpret_cast<float*>(workspace);
+  const int grid = (int)norm_grad_parts(M);
+  const bool db = dy_dtype == BL_BF16;
+  if (x_dtype < 0)
+    BL_TRY((db ? launch_norm_grad<__nv_bfloat16, int8_t> : launch_norm_grad<float, int8_t>)(
+        p, dx_dtype, grid, st));
+  else if (x_dtype == BL_BF16)
+    BL_TRY((db ? launch_norm_grad<__nv_bfloat16, __nv_bfloat16>
+               : launch_norm_grad<float, __nv_bfloat16>)(p, dx_dtype, grid, st));
+  else
+    BL_TRY((db ? launch_norm_grad<__nv_bfloat16, float> : launch_norm_grad<float, float>)(
+        p, dx_dtype, grid, st));
+  norm_colsum_kernel<<<(unsigned)((2 * K + 255) / 256), 256, 0, st>>>(p.part, grid, K, dweight, dbias);
+  BL_CUDA(cudaGetLastError());
+  return BL_OK;
 }
 
 inline int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
@@ -1691,6 +1813,279 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
   p.mask_gamma = gamma;
   p.eps = eps;
   return run_bf16_gemm(dyb, N, ahb, K, p, kMajAMN | kMajBMN, dev, st);
+}
+
+// ---------------------------------------------------------------------------
+// 4-bit weights with group scales.
+
+size_t bl_w4_bytes(int64_t N, int64_t K) {
+  return N > 0 && K > 0 ? w4_blocks(N, K) * 1024 : 0;
+}
+
+int64_t bl_w4_scale_count(int64_t N, int64_t K, int group) {
+  return N > 0 && K > 0 && check_group(group) == BL_OK ? (int64_t)w4_blocks(N, K) * 16 * (128 / group)
+                                                       : 0;
+}
+
+bl_status bl_quant_weights_w4(const void* W, bl_dtype w_dtype, int64_t N, int64_t K, int group,
+                              uint8_t* W4, void* scales, uint8_t* zeros, bl_stream_t stream) {
+  BL_TRY(check_dtype(w_dtype));
+  BL_TRY(check_k(K));
+  BL_TRY(check_rows(N));
+  BL_TRY(check_group(group));
+  if (N == 0) return BL_OK;
+  BL_TRY(check_ptr(W));
+  BL_TRY(check_ptr(W4));
+  BL_TRY(check_ptr(scales));
+  if (zeros != nullptr) BL_TRY(check_ptr(zeros));
+  int dev, sms;
+  BL_TRY(current_device(&dev, &sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = loop_grid((int64_t)w4_blocks(N, K) * 16, 16, sms);
+  uint32_t* out = reinterpret_cast<uint32_t*>(W4);
+  __nv_bfloat16* sc = reinterpret_cast<__nv_bfloat16*>(scales);
+  if (w_dtype == BL_BF16)
+    w4_quant_kernel<<<grid, 256, 0, st>>>(reinterpret_cast<const __nv_bfloat16*>(W), N, K, group,
+                                          out, sc, zeros);
+  else
+    w4_quant_kernel<<<grid, 256, 0, st>>>(reinterpret_cast<const float*>(W), N, K, group, out, sc,
+                                          zeros);
+  BL_CUDA(cudaGetLastError());
+  return BL_OK;
+}
+
+bl_status bl_pack_w4(const uint8_t* codes, const void* scales_in, const uint8_t* zeros_in, int64_t N,
+                     int64_t K, int group, uint8_t* W4, void* scales, uint8_t* zeros,
+                     bl_stream_t stream) {
+  BL_TRY(check_k(K));
+  BL_TRY(check_rows(N));
+  BL_TRY(check_group(group));
+  if ((zeros_in == nullptr) != (zeros == nullptr)) return BL_ERR_INVALID_ARG;
+  if (N == 0) return BL_OK;
+  BL_TRY(check_ptr(codes));
+  BL_TRY(check_ptr(scales_in));
+  BL_TRY(check_ptr(W4));
+  BL_TRY(check_ptr(scales));
+  if (zeros != nullptr) {
+    BL_TRY(check_ptr(zeros_in));
+    BL_TRY(check_ptr(zeros));
+  }
+  int dev, sms;
+  BL_TRY(current_device(&dev, &sms));
+  w4_pack_kernel<<<loop_grid((int64_t)w4_blocks(N, K) * 256, 256, sms), 256, 0,
+                   reinterpret_cast<cudaStream_t>(stream)>>>(
+      reinterpret_cast<const uint32_t*>(codes), reinterpret_cast<const __nv_bfloat16*>(scales_in),
+      zeros_in, N, K, group, reinterpret_cast<uint32_t*>(W4),
+      reinterpret_cast<__nv_bfloat16*>(scales), zeros);
+  BL_CUDA(cudaGetLastError());
+  return BL_OK;
+}
+
+bl_status bl_unpack_w4(const uint8_t* W4, const void* scales, const uint8_t* zeros, int64_t N,
+                       int64_t K, int group, void* W, bl_dtype w_dtype, bl_stream_t stream) {
+  BL_TRY(check_dtype(w_dtype));
+  BL_TRY(check_k(K));
+  BL_TRY(check_rows(N));
+  BL_TRY(check_group(group));
+  if (N == 0) return BL_OK;
+  BL_TRY(check_ptr(W4));
+  BL_TRY(check_ptr(scales));
+  if (zeros != nullptr) BL_TRY(check_ptr(zeros));
+  BL_TRY(check_ptr(W));
+  int dev, sms;
+  BL_TRY(current_device(&dev, &sms));
+  w4_unpack_kernel<<<loop_grid((int64_t)w4_blocks(N, K) * 256, 256, sms), 256, 0,
+                     reinterpret_cast<cudaStream_t>(stream)>>>(
+      reinterpret_cast<const uint32_t*>(W4), reinterpret_cast<const __nv_bfloat16*>(scales), zeros,
+      N, K, group, W, w_dtype == BL_BF16);
+  BL_CUDA(cudaGetLastError());
+  return BL_OK;
+}
+
+bl_status bl_linear_w4(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, const uint8_t* W4,
+                       const void* scales, const uint8_t* zeros, int64_t N, int group, void* Y,
+                       bl_dtype y_dtype, unsigned flags, bl_stream_t stream) {
+  BL_TRY(check_dtype(x_dtype));
+  BL_TRY(check_dtype(y_dtype));
+  BL_TRY(check_k(K));
+  BL_TRY(check_rows(M));
+  BL_TRY(check_rows(N));
+  BL_TRY(check_group(group));
+  if ((flags & ~(unsigned)BL_FLAG_PDL) != 0) return BL_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return BL_OK;
+  BL_TRY(check_ptr(X));
+  BL_TRY(check_ptr(W4));
+  BL_TRY(check_ptr(scales));
+  if (zeros != nullptr) BL_TRY(check_ptr(zeros));
+  BL_TRY(check_ptr(Y));
+  int dev, sms;
+  BL_TRY(current_device(&dev, &sms));
+  W4Params p = {};
+  p.X = X;
+  p.W4 = W4;
+  p.scales = reinterpret_cast<const __nv_bfloat16*>(scales);
+  p.zeros = zeros;
+  p.Y = Y;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.y_bf16 = y_dtype == BL_BF16;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return x_dtype == BL_BF16 ? launch_w4<__nv_bfloat16>(p, group, st) : launch_w4<float>(p, group, st);
+}
+
+// ---------------------------------------------------------------------------
+// Layer norm and 8-bit activation checkpoints.
+
+bl_status bl_layernorm(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, const float* weight,
+                       const float* bias, float eps, void* Y, bl_dtype y_dtype, float* mean,
+                       float* rstd, bl_stream_t stream) {
+  BL_TRY(check_dtype(x_dtype));
+  BL_TRY(check_dtype(y_dtype));
+  BL_TRY(check_k(K));
+  BL_TRY(check_rows(M));
+  BL_TRY(check_eps(eps));
+  if (M == 0) return BL_OK;
+  BL_TRY(check_ptr(X));
+  BL_TRY(check_ptr(weight));
+  if (bias != nullptr) BL_TRY(check_ptr(bias));
+  BL_TRY(check_ptr(Y));
+  if (mean != nullptr) BL_TRY(check_ptr(mean));
+  if (rstd != nullptr) BL_TRY(check_ptr(rstd));
+  int dev, sms;
+  BL_TRY(current_device(&dev, &sms));
+  NormParams p = {};
+  p.X = X;
+  p.weight = weight;
+  p.bias = bias;
+  p.M = M;
+  p.K = K;
+  p.eps = eps;
+  p.Y = Y;
+  p.mean = mean;
+  p.rstd = rstd;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int out = y_dtype == BL_BF16 ? 1 : 0;
+  return x_dtype == BL_BF16 ? launch_norm<__nv_bfloat16>(p, out, st) : launch_norm<float>(p, out, st);
+}
+
+bl_status bl_layernorm_quant(const void* X, bl_dtype x_dtype, int64_t M, int64_t K,
+                             const float* weight, const float* bias, float eps, float q_eps,
+                             int8_t* A_q, float* gamma_A, int32_t* rowsum, float* rstd,
+                             int8_t* xhat_q, float* xhat_scale, bl_stream_t stream) {
+  BL_TRY(check_dtype(x_dtype));
+  BL_TRY(check_k(K));
+  BL_TRY(check_rows(M));
+  BL_TRY(check_eps(eps));
+  BL_TRY(check_eps(q_eps));
+  if ((xhat_q == nullptr) != (xhat_scale == nullptr)) return BL_ERR_INVALID_ARG;
+  if (M == 0) return BL_OK;
+  BL_TRY(check_ptr(X));
+  BL_TRY(check_ptr(weight));
+  if (bias != nullptr) BL_TRY(check_ptr(bias));
+  BL_TRY(check_ptr(A_q));
+  BL_TRY(check_ptr(gamma_A));
+  if (rowsum != nullptr) BL_TRY(check_ptr(rowsum));
+  if (rstd != nullptr) BL_TRY(check_ptr(rstd));
+  if (xhat_q != nullptr) {
+    BL_TRY(check_ptr(xhat_q));
+    BL_TRY(check_ptr(xhat_scale));
+  }
+  int dev, sms;
+  BL_TRY(current_device(&dev, &sms));
+  NormParams p = {};
+  p.X = X;
+  p.weight = weight;
+  p.bias = bias;
+  p.M = M;
+  p.K = K;
+  p.eps = eps;
+  p.q_eps = q_eps;
+  p.rstd = rstd;
+  p.Aq = A_q;
+  p.gamma = gamma_A;
+  p.rowsum = rowsum;
+  p.xq = xhat_q;
+  p.xs = xhat_scale;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return x_dtype == BL_BF16 ? launch_norm<__nv_bfloat16>(p, 2, st) : launch_norm<float>(p, 2, st);
+}
+
+size_t bl_layernorm_grad_workspace_bytes(int64_t M, int64_t K) {
+  return M > 0 && K > 0 ? (size_t)norm_grad_parts(M) * 2 * (size_t)K * 4 : 0;
+}
+
+bl_status bl_layernorm_grad(const void* dY, bl_dtype dy_dtype, const void* X, bl_dtype x_dtype,
+                            const float* mean, const float* rstd, const float* weight, int64_t M,
+                            int64_t K, void* dX, bl_dtype dx_dtype, float* dweight, float* dbias,
+                            void* workspace, size_t ws_bytes, bl_stream_t stream) {
+  BL_TRY(check_dtype(x_dtype));
+  return norm_grad_impl(dY, dy_dtype, X, (int)x_dtype, nullptr, mean, rstd, weight, M, K, dX,
+                        dx_dtype, dweight, dbias, workspace, ws_bytes, stream);
+}
+
+bl_status bl_layernorm_grad_q8(const void* dY, bl_dtype dy_dtype, const int8_t* xhat_q,
+                               const float* xhat_scale, const float* rstd, const float* weight,
+                               int64_t M, int64_t K, void* dX, bl_dtype dx_dtype, float* dweight,
+                               float* dbias, void* workspace, size_t ws_bytes, bl_stream_t stream) {
+  return norm_grad_impl(dY, dy_dtype, xhat_q, -1, xhat_scale, nullptr, rstd, weight, M, K, dX,
+                        dx_dtype, dweight, dbias, workspace, ws_bytes, stream);
+}
+
+bl_status bl_relu2_requant_q8(const int32_t* acc_up, const float* gamma_x, const float* gamma_up,
+                              int64_t M, int64_t H, float eps, int8_t* R_q, float* gamma_r,
+                              int32_t* rowsum, uint8_t* P_q, float* p_scale, bl_stream_t stream) {
+  BL_TRY(check_k(H));
+  BL_TRY(check_rows(M));
+  BL_TRY(check_eps(eps));
+  if (M == 0) return BL_OK;
+  BL_TRY(check_ptr(acc_up));
+  BL_TRY(check_ptr(gamma_x));
+  if (gamma_up == nullptr) return BL_ERR_INVALID_ARG;
+  BL_TRY(check_ptr(R_q));
+  BL_TRY(check_ptr(gamma_r));
+  if (rowsum != nullptr) BL_TRY(check_ptr(rowsum));
+  BL_TRY(check_ptr(P_q));
+  BL_TRY(check_ptr(p_scale));
+  int dev, sms;
+  BL_TRY(current_device(&dev, &sms));
+  relu2_requant_q8_kernel<<<(unsigned)M, kNormThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      acc_up, H, gamma_x, gamma_up, eps, R_q, gamma_r, rowsum, P_q, p_scale);
+  BL_CUDA(cudaGetLastError());
+  return BL_OK;
+}
+
+bl_status bl_relu2_grad_q8(const void* dR, bl_dtype dr_dtype, const uint8_t* P_q,
+                           const float* p_scale, int64_t M, int64_t H, void* dH, bl_dtype dh_dtype,
+                           bl_stream_t stream) {
+  BL_TRY(check_dtype(dr_dtype));
+  BL_TRY(check_dtype(dh_dtype));
+  BL_TRY(check_k(H));
+  BL_TRY(check_rows(M));
+  if (M == 0) return BL_OK;
+  BL_TRY(check_ptr(dR));
+  BL_TRY(check_ptr(P_q));
+  BL_TRY(check_ptr(p_scale));
+  BL_TRY(check_ptr(dH));
+  int dev, sms;
+  BL_TRY(current_device(&dev, &sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t units = M * (H / 8);
+  const unsigned grid = loop_grid(units, kNormThreads, sms);
+  const float* df = reinterpret_cast<const float*>(dR);
+  const __nv_bfloat16* db = reinterpret_cast<const __nv_bfloat16*>(dR);
+  float* of = reinterpret_cast<float*>(dH);
+  __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(dH);
+  if (dr_dtype == BL_BF16 && dh_dtype == BL_BF16)
+    relu2_grad_q8_kernel<<<grid, kNormThreads, 0, st>>>(db, P_q, p_scale, units, ob);
+  else if (dr_dtype == BL_BF16)
+    relu2_grad_q8_kernel<<<grid, kNormThreads, 0, st>>>(db, P_q, p_scale, units, of);
+  else if (dh_dtype == BL_BF16)
+    relu2_grad_q8_kernel<<<grid, kNormThreads, 0, st>>>(df, P_q, p_scale, units, ob);
+  else
+    relu2_grad_q8_kernel<<<grid, kNormThreads, 0, st>>>(df, P_q, p_scale, units, of);
+  BL_CUDA(cudaGetLastError());
+  return BL_OK;
 }
 
 bl_status bl_check_device_error(bl_stream_t stream) {

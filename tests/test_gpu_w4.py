@@ -1,0 +1,198 @@
+"""4-bit weights with group scales through the C ABI: the quantiser and the
+packing bit for bit, the product against 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import w4_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def bl():
+    import ternary_weight_linear_absmax_b200 as m
+    m.load()
+    return m
+
+
+def _weights(N, K, seed, dt):
+    rng = np.random.default_rng(seed)
+    W = (rng.standard_normal((N, K)) * 0.02).astype(np.float32)
+    W[0, :min(K, 32)] = 0.0                       # an empty group
+    if N > 2:
+        W[2] = np.abs(W[2])                       # one sign only
+    return torch.from_numpy(W).to(ref.KINDS[dt])
+
+
+def _unpacked(bl, W4, scales, zp, N, K):
+    return bl.bl_unpack_w4(W4, scales, N, K, zeros=zp).cpu().numpy().astype(np.float64)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("N,K,group", [(1, 64, 32), (16, 128, 128), (37, 192, 128), (50, 320, 64),
+                                       (33, 1088, 32)])
+def test_quantiser_bit_exact(bl, N, K, group, zeros, dt):
+    W = _weights(N, K, N + K, dt)
+    W4, scales, zp = bl.bl_quant_weights_w4(W.to(DEV), group, zeros=zeros)
+    codes, s, z = ref.quant_w4(W.float().numpy(), group, zeros)
+    words, sc, zpr = ref.pack(codes, s, z, group, zeros)
+    got = W4.cpu().numpy().view(np.uint32).reshape(words.shape)
+    rows = np.zeros((words.shape[0] * 16, words.shape[1] * 128), bool)
+    rows[:N, :K] = True
+    inside = rows.reshape(words.shape[0], 2, 8, words.shape[1], 4, 4, 8).all(-1).transpose(0, 3, 1, 2, 5, 4)
+    np.testing.assert_array_equal(got[inside], words[inside])
+    np.testing.assert_array_equal(_unpacked(bl, W4, scales, zp, N, K), ref.dequant(codes, s, z, group))
+    # what lies outside the matrix has scale 0
+    full = scales.float().cpu().numpy()
+    np.testing.assert_array_equal(full, sc)
+    assert (zp is None) == (not zeros)
+    # the same codes through bl_pack_w4
+    nib = (codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8)
+    P4, psc, pzp = bl.bl_pack_w4(torch.from_numpy(nib).to(DEV), torch.from_numpy(s).bfloat16().to(DEV), group,
+                                 zeros=torch.from_numpy(z.astype(np.uint8)).to(DEV) if zeros else None)
+    np.testing.assert_array_equal(P4.cpu().numpy().view(np.uint32).reshape(words.shape)[inside], words[inside])
+    np.testing.assert_array_equal(psc.float().cpu().numpy(), sc)
+    np.testing.assert_array_equal(_unpacked(bl, P4, psc, pzp, N, K), ref.dequant(codes, s, z, group))
+    half = bl.bl_unpack_w4(W4, scales, N, K, zeros=zp, out_dtype=torch.bfloat16).float().cpu().numpy()
+    np.testing.assert_array_equal(half, ref.bf16(ref.dequant(codes, s, z, group)))
+
+
+def test_quantiser_borders(bl):
+    """Values on, just below and just above (k + 1/2)·s, and scales from the
+    smallest bf16 up: ties go to the even code, neighbours to their side."""
+    rows = []
+    for s in (np.float32(2.0 ** -7), np.float32(0.0078735352), np.float32(2.0 ** -126), np.float32(2.0 ** -132)):
+        b = ((np.arange(-7, 7) + 0.5) * np.float64(s)).astype(np.float32)
+        row = np.concatenate([b, np.nextafter(b, np.float32(np.inf)), np.nextafter(b, np.float32(-np.inf)),
+                              [7 * s, -7 * s], np.zeros(20, np.float32)]).astype(np.float32)
+        rows.append(row[:64])
+    rows.append(np.full(64, 2.0 ** -149, np.float32))   # below every bf16: scale 0
+    W = np.stack(rows)
+    for zeros in (False, True):
+        codes, s, z = ref.quant_w4(W, 64, zeros)
+        W4, scales, zp = bl.bl_quant_weights_w4(torch.from_numpy(W).to(DEV), 64, zeros=zeros)
+        np.testing.assert_array_equal(_unpacked(bl, W4, scales, zp, *W.shape), ref.dequant(codes, s, z, 64))
+
+
+def _problem(bl, M, N, K, group, zeros, dt, seed):
+    rng = np.random.default_rng(seed)
+    G = -(-K // group)
+    codes = rng.integers(0, 16, (N, K))
+    s = ref.bf16(rng.uniform(0.002, 0.01, (N, G)).astype(np.float32))
+    z = rng.integers(0, 16, (N, G)) if zeros else np.full((N, G), 8)
+    nib = (codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8)
+    packed = bl.bl_pack_w4(torch.from_numpy(nib).to(DEV), torch.from_numpy(s).bfloat16().to(DEV), group,
+                           zeros=torch.from_numpy(z.astype(np.uint8)).to(DEV) if zeros else None)
+    X = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32)).to(ref.KINDS[dt])
+    return X, packed, ref.dequant(codes, s, z, group)
+
+
+def _check(bl, M, N, K, group, zeros, xdt, ydt, seed=0):
+    X, (W4, sc, zp), w = _problem(bl, M, N, K, group, zeros, xdt, seed)
+    Y = bl.bl_linear_w4(X.to(DEV), W4, sc, N, zeros=zp, out_dtype=ref.KINDS[ydt])
+    x = X.double().numpy()
+    want = x @ w.T
+    got = Y.double().cpu().numpy()
+    tol = ref.linear_bound(x, w, K, ydt == "bf16", want)
+    assert got.shape == want.shape
+    assert np.all(np.abs(got - want) <= tol), np.max(np.abs(got - want) / tol)
+
+
+@pytest.mark.parametrize("M,N,K,group,zeros,xdt,ydt", [
+    (1, 1, 64, 32, False, "bf16", "f32"), (1, 16, 128, 128, True, "f32", "f32"),
+    (2, 17, 192, 64, True, "bf16", "bf16"), (3, 250, 512, 32, False, "f32", "bf16"),
+    (4, 256, 512, 32, True, "f32", "f32"), (5, 129, 448, 128, False, "f32", "f32"),
+    (7, 100, 1088, 64, False, "bf16", "f32"), (8, 333, 2560, 128, True, "bf16", "bf16"),
+    (9, 64, 4096, 32, True, "bf16", "f32"), (11, 48, 704, 32, False, "f32", "f32"),
+    (16, 555, 1024, 64, True, "bf16", "bf16"), (17, 40, 640, 128, False, "bf16", "f32"),
+    (33, 70, 576, 64, True, "f32", "bf16"), (64, 96, 1280, 128, True, "bf16", "f32"),
+    (65, 31, 320, 32, False, "bf16", "f32"), (130, 20, 192, 64, True, "f32", "f32")])
+def test_linear(bl, M, N, K, group, zeros, xdt, ydt):
+    _check(bl, M, N, K, group, zeros, xdt, ydt, seed=M * N)
+
+
+@pytest.mark.parametrize("M,N,K,group", [(1, 6912, 2560, 128), (2, 300, 37440, 64), (1, 40, 262144, 128),
+                                         (16, 11008, 1024, 64), (1, 20011, 512, 32)])
+def test_linear_long(bl, M, N, K, group):
+    """The decode matrix, long rows and many rows."""
+    _check(bl, M, N, K, group, True, "bf16", "f32", seed=K)
+
+
+def test_linear_seeded_shapes(bl):
+    rng = np.random.default_rng(7)
+    for i in range(24):
+        M, N, K = int(rng.integers(1, 40)), int(rng.integers(1, 700)), 64 * int(rng.integers(1, 40))
+        _check(bl, M, N, K, int(rng.choice([32, 64, 128])), bool(rng.integers(2)),
+               ["bf16", "f32"][rng.integers(2)], ["bf16", "f32"][rng.integers(2)], seed=i)
+
+
+def test_fp32_values_of_all_sizes(bl):
+    """An fp32 activation keeps its 24 bits, from the smallest values to the
+    largest that the sum allows."""
+    K, N = 64, 16
+    X, (W4, sc, zp), w = _problem(bl, 4, N, K, 32, False, "f32", 3)
+    x = X.numpy() * np.array([1e-30, 1.0, 1e30, 3e37], np.float32)[:, None]
+    x[0, 0], x[1, 1], x[3] = 1.17549435e-38, 1 + 2.0 ** -23, 0
+    x[3, 5] = 3.4e38
+    got = bl.bl_linear_w4(torch.from_numpy(x).to(DEV), W4, sc, N, out_dtype=torch.float32)
+    want = x.astype(np.float64) @ w.T
+    tol = ref.linear_bound(x.astype(np.float64), w, K, False, want)
+    assert np.all(np.abs(got.double().cpu().numpy() - want) <= tol)
+
+
+def test_empty_and_outputs_untouched(bl):
+    X, (W4, sc, zp), w = _problem(bl, 3, 21, 192, 64, True, "bf16", 5)
+    Xd = X.to(DEV)
+    assert bl.bl_linear_w4(Xd[:0], W4, sc, 21, zeros=zp).shape == (0, 21)
+    # the buffer behind the output stays as it was
+    buf = torch.full((3 * 21 + 64,), 7.0, device=DEV)
+    out = buf[:63].view(3, 21)
+    bl.bl_linear_w4(Xd, W4, sc, 21, zeros=zp, out=out)
+    assert torch.all(buf[63:] == 7.0)
+    assert torch.equal(out, bl.bl_linear_w4(Xd, W4, sc, 21, zeros=zp, out_dtype=torch.float32))
+
+
+def test_nan_outside_the_matrix_is_not_read(bl):
+    """Rows past N and columns past K never reach a result, whatever their
+    codes; scales there are 0 by construction."""
+    N, K = 5, 64
+    X, (W4, sc, zp), w = _problem(bl, 2, N, K, 32, False, "bf16", 6)
+    base = bl.bl_linear_w4(X.to(DEV), W4, sc, N, out_dtype=torch.float32)
+    words = W4.view(-1, 2, 8, 4, 4, 4)
+    words[:, :, :, :, 2:] = 0xFF                   # columns 64..127
+    words[:, 1] = 0xFF                             # rows 8..15
+    assert torch.equal(base, bl.bl_linear_w4(X.to(DEV), W4, sc, N, out_dtype=torch.float32))
+
+
+def test_streams_graph_and_repeat(bl):
+    """On a side stream, in a captured and replayed graph, and with programmatic
+    dependent launch in a chain: the same bits as the plain call."""
+    N, K = 4096, 4096
+    X, (W4, sc, zp), w = _problem(bl, 2, N, K, 128, True, "bf16", 8)
+    X = X.to(DEV)
+    base = bl.bl_linear_w4(X, W4, sc, N, zeros=zp)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = bl.bl_linear_w4(X, W4, sc, N, zeros=zp, stream=side)
+    side.synchronize()
+    assert torch.equal(base, other)
+    out = torch.empty_like(base)
+    chain = [torch.empty_like(base) for _ in range(4)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        h = X
+        for c in chain:
+            bl.bl_linear_w4(h, W4, sc, N, zeros=zp, out=c, pdl=True)
+            h = c
+        bl.bl_linear_w4(X, W4, sc, N, zeros=zp, out=out, pdl=True)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(base, out) and torch.equal(base, chain[0])
+    h = X
+    for c in chain:
+        h = bl.bl_linear_w4(h, W4, sc, N, zeros=zp)
+        assert torch.equal(h, c)
