@@ -858,19 +858,87 @@ inline unsigned loop_grid(int64_t items, int64_t per, int sms) {
   return (unsigned)(b < 1 ? 1 : b);
 }
 
-template <typename T>
-bl_status launch_w4(const W4Params& p, int group, cudaStream_t st) {
-  const int64_t tok = sizeof(T) == 2 ? 8 : 2;
-  const int64_t gy = (p.M + tok - 1) / tok;
-  const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)(gy < 65535 ? gy : 65535));
-  if (group == 32)
-    w4_linear_kernel<T, 32><<<grid, kW4Threads, 0, st>>>(p);
-  else if (group == 64)
-    w4_linear_kernel<T, 64><<<grid, kW4Threads, 0, st>>>(p);
-  else
-    w4_linear_kernel<T, 128><<<grid, kW4Threads, 0, st>>>(p);
-  BL_CUDA(cudaGetLastError());
+// Warps per row block. A CTA's 16 warps form 16/split groups, each taking a
+// row block of the slab at a time, so a slab of n row blocks takes
+// ceil(n/(16/split)) rounds of ceil(KB/split) blocks; the end of a row block
+// (sums through shared memory, the store) is worth about three blocks.
+int w4_split(int64_t slab, int64_t KB) {
+  int best = 1;
+  int64_t cost = 0;
+  for (int s = 1; s <= kW4Warps; s *= 2) {
+    const int64_t groups = kW4Warps / s;
+    const int64_t c = (slab + groups - 1) / groups * ((KB + s - 1) / s + 3);
+    if (s == 1 || c < cost) {
+      best = s;
+      cost = c;
+    }
+  }
+  return best;
+}
+
+template <typename T, int V, int NT>
+bl_status launch_w4_nt(W4Params p, bool pdl, int dev, int sms, cudaStream_t st) {
+  constexpr int P = sizeof(T) == 2 ? 1 : 3, TOK = 8 * NT / P;
+  const size_t xs = (size_t)((p.M < TOK ? p.M : TOK) * P) * w4_x_stride(p.K);
+  // as many blocks in flight as shared memory holds beside the activations
+  int depth = 8;
+  while (depth > 2 && w4_fixed_bytes<V, NT>(depth) + xs > kW4SmemCap) depth /= 2;
+  const bool fits = w4_fixed_bytes<V, NT>(depth) + xs <= kW4SmemCap;
+  if (!fits) depth = 8;
+  while (w4_fixed_bytes<V, NT>(depth) > kW4SmemCap) depth /= 2;
+  const size_t smem = w4_fixed_bytes<V, NT>(depth) + (fits ? xs : 0);
+  auto* k = fits ? w4_linear_kernel<T, V, NT, true> : w4_linear_kernel<T, V, NT, false>;
+  BL_TRY(ensure_smem(k, dev, smem));
+  const int64_t RB = (p.N + 15) / 16, grid = RB < sms ? RB : sms;
+  p.depth = depth;
+  p.split = w4_split((RB + grid - 1) / grid, (p.K + 127) / 128);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)((p.M + TOK - 1) / TOK));
+  cfg.blockDim = dim3(kW4Threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  BL_CUDA(cudaLaunchKernelEx(&cfg, k, p));
   return BL_OK;
+}
+
+template <int V, int NT>
+bool w4_fits(size_t x_bytes) {
+  return w4_fixed_bytes<V, NT>(2) + x_bytes <= kW4SmemCap;
+}
+// MMA columns a launch takes at once: 8, 16 or 32, as many as the tokens need
+// and shared memory holds.
+template <typename T, int V>
+bl_status launch_w4_v(W4Params p, bool pdl, int dev, int sms, cudaStream_t st) {
+  constexpr int64_t P = sizeof(T) == 2 ? 1 : 3;
+  // grid.y holds 65,535 passes; longer calls go in parts
+  const int64_t part = (int64_t)65535 * (8 / P);
+  for (int64_t m = 0, M = p.M; m < M; m += part) {
+    W4Params q = p;
+    q.X = reinterpret_cast<const T*>(p.X) + m * p.K;
+    q.Y = reinterpret_cast<uint8_t*>(p.Y) + m * p.N * (p.y_bf16 ? 2 : 4);
+    q.M = M - m < part ? M - m : part;
+    const int64_t cols = q.M * P;
+    const size_t x = w4_x_stride(p.K);
+    if (cols <= 8 || (w4_fits<V, 1>(8 * x) && !w4_fits<V, 2>(16 * x)))
+      BL_TRY((launch_w4_nt<T, V, 1>(q, pdl, dev, sms, st)));
+    else if (cols <= 16 || (w4_fits<V, 2>(16 * x) && !w4_fits<V, 4>(32 * x)))
+      BL_TRY((launch_w4_nt<T, V, 2>(q, pdl, dev, sms, st)));
+    else
+      BL_TRY((launch_w4_nt<T, V, 4>(q, pdl, dev, sms, st)));
+  }
+  return BL_OK;
+}
+
+template <typename T>
+bl_status launch_w4(const W4Params& p, int group, bool pdl, int dev, int sms, cudaStream_t st) {
+  if (group == 32) return launch_w4_v<T, 4>(p, pdl, dev, sms, st);
+  if (group == 64) return launch_w4_v<T, 2>(p, pdl, dev, sms, st);
+  return launch_w4_v<T, 1>(p, pdl, dev, sms, st);
 }
 
 // --------------------------------------------------------------------------
@@ -1930,8 +1998,11 @@ bl_status bl_linear_w4(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, co
   p.N = N;
   p.K = K;
   p.y_bf16 = y_dtype == BL_BF16;
+  p.ones = kW4Ones;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return x_dtype == BL_BF16 ? launch_w4<__nv_bfloat16>(p, group, st) : launch_w4<float>(p, group, st);
+  const bool pdl = (flags & BL_FLAG_PDL) != 0;
+  return x_dtype == BL_BF16 ? launch_w4<__nv_bfloat16>(p, group, pdl, dev, sms, st)
+                            : launch_w4<float>(p, group, pdl, dev, sms, st);
 }
 
 // ---------------------------------------------------------------------------
