@@ -466,10 +466,13 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
  *   bl_unpack_w4  the matrix [N, K] the packed weights stand for (exact in fp32;
  *     one rounding for bf16).
  *   bl_linear_w4  Y [M, N] = X·Wᵀ from fp32/bf16 activations [M, K], for few
- *     tokens (any M is taken; the weights are read again for every group of
- *     tokens a launch takes at once). Products are exact and
- *     the sums are fp32 (an fp32 X is split into three bf16 pieces whose sum it
- *     is). flags: BL_FLAG_PDL as for bl_linear_ex. */
+ *     tokens: up to 16 go through the weights at once, more in passes of 16.
+ *     K up to BL_W4_MAX_K. Per token and 128 columns the activations are taken
+ *     in fixed point, rounded to 2^-23 of the largest of them or less (what
+ *     aligning to it in an fp32 sum would lose); products and the sums of a
+ *     group are exact integers, the rest is fp32. An infinity or NaN makes its
+ *     token's results NaN. flags: BL_FLAG_PDL as for bl_linear_ex. */
+#define BL_W4_MAX_K 262144
 size_t bl_w4_bytes(int64_t N, int64_t K);
 int64_t bl_w4_scale_count(int64_t N, int64_t K, int group);
 bl_status bl_quant_weights_w4(const void* W, bl_dtype w_dtype, int64_t N, int64_t K, int group,

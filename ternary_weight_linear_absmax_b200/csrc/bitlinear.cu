@@ -858,78 +858,96 @@ inline unsigned loop_grid(int64_t items, int64_t per, int sms) {
   return (unsigned)(b < 1 ? 1 : b);
 }
 
-// Warps per row block. A CTA's 16 warps form 16/split groups, each taking a
-// row block of the slab at a time, so a slab of n row blocks takes
-// ceil(n/(16/split)) rounds of ceil(KB/split) blocks; the end of a row block
-// (sums through shared memory, the store) is worth about three blocks.
-int w4_split(int64_t slab, int64_t KB) {
-  int best = 1;
-  int64_t cost = 0;
-  for (int s = 1; s <= kW4Warps; s *= 2) {
-    const int64_t groups = kW4Warps / s;
-    const int64_t c = (slab + groups - 1) / groups * ((KB + s - 1) / s + 3);
-    if (s == 1 || c < cost) {
-      best = s;
-      cost = c;
-    }
-  }
-  return best;
-}
-
+#ifndef W4CTAS
+#define W4CTAS 2
+#endif
+// One launch: slabs × clusters. Returns BL_ERR_SHAPE where the activations of
+// a pass do not fit.
 template <typename T, int V, int NT>
 bl_status launch_w4_nt(W4Params p, bool pdl, int dev, int sms, cudaStream_t st) {
-  constexpr int P = sizeof(T) == 2 ? 1 : 3, TOK = 8 * NT / P;
-  const size_t xs = (size_t)((p.M < TOK ? p.M : TOK) * P) * w4_x_stride(p.K);
-  // as many blocks in flight as shared memory holds beside the activations
-  int depth = 8;
-  while (depth > 2 && w4_fixed_bytes<V, NT>(depth) + xs > kW4SmemCap) depth /= 2;
-  const bool fits = w4_fixed_bytes<V, NT>(depth) + xs <= kW4SmemCap;
-  if (!fits) depth = 8;
-  while (w4_fixed_bytes<V, NT>(depth) > kW4SmemCap) depth /= 2;
-  const size_t smem = w4_fixed_bytes<V, NT>(depth) + (fits ? xs : 0);
-  auto* k = fits ? w4_linear_kernel<T, V, NT, true> : w4_linear_kernel<T, V, NT, false>;
+  using C = W4Pass<NT>;
+  const int64_t RB = (p.N + 15) / 16, KB = (p.K + 127) / 128;
+  const int toks = (int)(p.M < C::kTok ? p.M : C::kTok);
+  // The smallest cluster, and the most ring stages with it, that fit.
+  const int64_t out_rows = (int64_t)(kW4OutCap / (64 * toks));
+  int ranks = 1, stages = 0;
+  size_t smem = 0;
+  int64_t slabs = 0;
+  for (; ranks <= kW4MaxCluster && stages == 0; ranks *= 2) {
+    const int64_t kb = (KB + ranks - 1) / ranks;
+    for (int s = kW4Stages; s >= (ranks < kW4MaxCluster ? 3 : 2); --s) {
+      // two CTAs per SM where two fit, as many slabs as there is room for them
+      for (int per_sm = NT == 1 ? W4CTAS : 1; per_sm >= 1; --per_sm) {
+        int64_t n = (int64_t)per_sm * sms / ranks;
+        if (n > RB) n = RB;
+        if (n * out_rows < RB) n = (RB + out_rows - 1) / out_rows;
+        if (3 * toks * kb * 128 > (int64_t)kW4SmemCap) continue;
+        const size_t need = w4_smem<V, NT>((int)kb, (int)((RB + n - 1) / n), toks, s).total;
+        if (need > (per_sm == 2 ? 113 * 1024 : kW4SmemCap)) continue;
+        stages = s;
+        smem = need;
+        slabs = n;
+        break;
+      }
+      if (stages != 0) break;
+    }
+    if (stages != 0) break;
+  }
+  if (stages == 0) return BL_ERR_SHAPE;
+  auto* k = w4_linear_kernel<T, V, NT>;
   BL_TRY(ensure_smem(k, dev, smem));
-  const int64_t RB = (p.N + 15) / 16, grid = RB < sms ? RB : sms;
-  p.depth = depth;
-  p.split = w4_split((RB + grid - 1) / grid, (p.K + 127) / 128);
+  p.stages = stages;
+  p.slabs = (int)slabs;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)((p.M + TOK - 1) / TOK));
+  cfg.gridDim = dim3((unsigned)(slabs * ranks), (unsigned)((p.M + C::kTok - 1) / C::kTok));
   cfg.blockDim = dim3(kW4Threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  int attrs = 0;
+  if (pdl) {
+    attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[attrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (ranks > 1) {
+    attr[attrs].id = cudaLaunchAttributeClusterDimension;
+    attr[attrs].val.clusterDim.x = (unsigned)ranks;
+    attr[attrs].val.clusterDim.y = 1;
+    attr[attrs++].val.clusterDim.z = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cfg.numAttrs = attrs;
   BL_CUDA(cudaLaunchKernelEx(&cfg, k, p));
   return BL_OK;
 }
 
-template <int V, int NT>
-bool w4_fits(size_t x_bytes) {
-  return w4_fixed_bytes<V, NT>(2) + x_bytes <= kW4SmemCap;
-}
-// MMA columns a launch takes at once: 8, 16 or 32, as many as the tokens need
-// and shared memory holds.
+// Tokens a launch takes at once: 2, 5, 8 or 16 per pass, fewer where the
+// activations of a pass do not fit.
 template <typename T, int V>
-bl_status launch_w4_v(W4Params p, bool pdl, int dev, int sms, cudaStream_t st) {
-  constexpr int64_t P = sizeof(T) == 2 ? 1 : 3;
+bl_status launch_w4_v(const W4Params& p, bool pdl, int dev, int sms, cudaStream_t st) {
   // grid.y holds 65,535 passes; longer calls go in parts
-  const int64_t part = (int64_t)65535 * (8 / P);
-  for (int64_t m = 0, M = p.M; m < M; m += part) {
+  const int64_t part = 2 * 65535;
+  for (int64_t m = 0; m < p.M; m += part) {
     W4Params q = p;
     q.X = reinterpret_cast<const T*>(p.X) + m * p.K;
     q.Y = reinterpret_cast<uint8_t*>(p.Y) + m * p.N * (p.y_bf16 ? 2 : 4);
-    q.M = M - m < part ? M - m : part;
-    const int64_t cols = q.M * P;
-    const size_t x = w4_x_stride(p.K);
-    if (cols <= 8 || (w4_fits<V, 1>(8 * x) && !w4_fits<V, 2>(16 * x)))
-      BL_TRY((launch_w4_nt<T, V, 1>(q, pdl, dev, sms, st)));
-    else if (cols <= 16 || (w4_fits<V, 2>(16 * x) && !w4_fits<V, 4>(32 * x)))
-      BL_TRY((launch_w4_nt<T, V, 2>(q, pdl, dev, sms, st)));
-    else
-      BL_TRY((launch_w4_nt<T, V, 4>(q, pdl, dev, sms, st)));
+    q.M = p.M - m < part ? p.M - m : part;
+    bl_status s = BL_ERR_SHAPE;
+    if (q.M > 8) s = launch_w4_nt<T, V, 6>(q, pdl, dev, sms, st);
+    if (q.M > 5 && s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 3>(q, pdl, dev, sms, st);
+    if (q.M > 2 && s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 2>(q, pdl, dev, sms, st);
+    if (s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 1>(q, pdl, dev, sms, st);
+    if (s == BL_ERR_SHAPE && q.M > 1) {  // two long rows do not fit: one by one
+      const int64_t M = q.M;
+      q.M = 1;
+      s = BL_OK;
+      for (int64_t i = 0; i < M && s == BL_OK; ++i) {
+        s = launch_w4_nt<T, V, 1>(q, pdl, dev, sms, st);
+        q.X = reinterpret_cast<const T*>(q.X) + p.K;
+        q.Y = reinterpret_cast<uint8_t*>(q.Y) + p.N * (p.y_bf16 ? 2 : 4);
+      }
+    }
+    BL_TRY(s);
   }
   return BL_OK;
 }
@@ -1979,6 +1997,7 @@ bl_status bl_linear_w4(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, co
   BL_TRY(check_rows(M));
   BL_TRY(check_rows(N));
   BL_TRY(check_group(group));
+  if (K > (int64_t)BL_W4_MAX_K) return BL_ERR_SHAPE;
   if ((flags & ~(unsigned)BL_FLAG_PDL) != 0) return BL_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return BL_OK;
   BL_TRY(check_ptr(X));
@@ -1998,7 +2017,6 @@ bl_status bl_linear_w4(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, co
   p.N = N;
   p.K = K;
   p.y_bf16 = y_dtype == BL_BF16;
-  p.ones = kW4Ones;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool pdl = (flags & BL_FLAG_PDL) != 0;
   return x_dtype == BL_BF16 ? launch_w4<__nv_bfloat16>(p, group, pdl, dev, sms, st)

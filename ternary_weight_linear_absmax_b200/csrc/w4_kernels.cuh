@@ -5,15 +5,15 @@
 //   w[n, k] = s[n, k/G] · (q[n, k] − z[n, k/G]),  q ∈ [0, 15], G ∈ {32, 64, 128},
 //   s bf16, z = 8 (symmetric) or stored, 0..15.
 //
-// Layout. A warp-level bf16 MMA (m16n8k16) takes 16 weight rows × 16 columns
+// Layout. A warp-level int8 MMA (m16n8k32) takes 16 weight rows × 32 columns
 // as its A operand: lane 4g + t holds rows g and g + 8. The packed matrix is
 // cut into blocks of 16 rows × 128 columns, 1024 bytes each, K blocks of a row
 // block one after the other. Word (h, g, t, u) of a block (u fastest) holds
 // row 16·rb + 8·h + g, columns 128·kb + 32·u + 8·t + (0..7), column 2·p + e of
 // those at bit 4·p + 16·e. So lane 4g + t reads 16 contiguous bytes per row
 // half (a warp reads 512 contiguous bytes), its four words lie in the four
-// 32-column groups of the block, and (word >> 4p) & 0x000F000F is the pair of
-// codes of two neighbouring columns in the two halves of a register.
+// 32-column groups of the block, and word & 0x0F0F0F0F, (word >> 4) &
+// 0x0F0F0F0F are its codes of columns (0, 4, 1, 5) and (2, 6, 3, 7) as bytes.
 // Scales and zero points are [rb, kb, g, 128/G, h]: a lane's are contiguous.
 // Rows past N and columns past K hold scale 0.
 #pragma once
@@ -30,115 +30,32 @@ struct W4Params {
   void* Y;                        // [M, N] fp32/bf16
   int64_t M, N, K;
   int y_bf16;
-  int split;                      // warps per row block: 1, 2, 4, 8 or 16
-  int depth;                      // blocks in flight per warp: 2, 4 or 8
-  uint32_t ones;                  // kW4Ones
+  int stages;                     // ring stages per warp: 2, 3 or 4
+  int slabs;                      // slabs of row blocks (grid.x = slabs × CTAs per cluster)
 };
 
-__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+__device__ __forceinline__ void mma_u8s8_16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                                uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The pair q of codes of a packed word as bf16 (q − z)/128, exact: 0x3F80 | q
-// is the bf16 1 + q/128 (7 mantissa bits), `one_z` holds 1 + z/128 twice. The
-// sums stay 128 times smaller until the result is written, so that no product
-// overflows whose scaled sum does not. `ones` is 0x3F803F80 in a register that
-// the compiler does not see through: with both constants known it takes two
-// logic operations per pair instead of one.
-constexpr float kW4Unit = 128.0f;
-constexpr uint32_t kW4Ones = 0x3F803F80u;
-__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int q, uint32_t ones, uint32_t one_z) {
-  uint32_t v;
-  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(word >> (4 * q)), "r"(ones));
-  uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(one_z));
-  return d;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Eight consecutive activations. A bf16 row is taken as it is; an fp32 value
-// is the exact sum of three bf16 pieces, each the leading 8 bits of what the
-// ones before left (cut, not rounded: 3 × 8 bits hold the 24-bit significand,
-// and no piece overflows), one per MMA column, so the products stay exact and
-// the sum is an fp32 sum.
-template <typename T>
-struct W4Eight {
-  float v[8];
-  __device__ __forceinline__ void load(const T* p) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-  }
-  // The next piece, as bf16 pairs; what it leaves stays for the one after.
-  __device__ __forceinline__ uint4 piece() {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[j] = __fsub_rn(v[j], __uint_as_float(__float_as_uint(v[j]) & 0xFFFF0000u));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <>
-struct W4Eight<__nv_bfloat16> {
-  uint4 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void clear() { v = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ uint4 piece() { return v; }
-};
-
-constexpr int kW4Warps = 16;
-constexpr int kW4Threads = 32 * kW4Warps;
-constexpr size_t kW4SmemCap = 226 * 1024;
-
-// Shared memory: the sums [2][warp][16 rows][8·NT],
-// each warp's ring of blocks (codes, scales, zero points), the activations.
-template <int NT>
-__host__ __device__ constexpr size_t w4_part_bytes() {
-  return (size_t)2 * kW4Warps * 16 * 8 * NT * 4;
-}
-template <int V>
-__host__ __device__ constexpr int w4_stage_bytes() {
-  return 1024 + 48 * V;
-}
-template <int V, int NT>
-__host__ __device__ constexpr size_t w4_fixed_bytes(int depth) {
-  return w4_part_bytes<NT>() + (size_t)kW4Warps * depth * w4_stage_bytes<V>();
-}
-// One MMA column of activations: KB blocks of 256 bytes and 64 more, so that
-// two columns (the eight lanes of a 16-byte read) fall on different banks.
-__host__ __device__ inline size_t w4_x_stride(int64_t K) { return (size_t)((K + 127) / 128) * 256 + 64; }
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
-}
-// The load where `on` holds, `v` as it was elsewhere.
-__device__ __forceinline__ void lds128_if(uint4& v, uint32_t a, bool on) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-               "@p ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "r"(a), "r"((int)on));
 }
 __device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
   uint32_t v;
@@ -150,214 +67,424 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float at `addr` of this CTA's shared memory, read from CTA `rank` of the cluster.
+__device__ __forceinline__ float cluster_lds_f32(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
 }
 
-// Y = X·Wᵀ for up to 8·NT MMA columns (tokens, or three pieces of an fp32
-// token) per grid row. Each CTA owns a slab of 16-row blocks. Groups of
-// `split` warps take a row block each, its 128-column blocks in turn, `depth`
-// blocks in flight per warp; the warps' sums meet in shared memory, in a
-// fixed order. XS: the activations lie in shared memory (each CTA reads them
-// once), else they are read through L2 (long rows).
-template <typename T, int V, int NT, bool XS>
-__global__ void __launch_bounds__(kW4Threads) w4_linear_kernel(const W4Params p) {
-  constexpr int P = sizeof(T) == 2 ? 1 : 3;     // MMA columns per token
-  constexpr int COLS = 8 * NT, TOK = COLS / P;  // tokens per pass
-  constexpr int ST = w4_stage_bytes<V>();
+constexpr int kW4Warps = 16;
+constexpr int kW4Threads = 32 * kW4Warps;
+constexpr int kW4Stages = 4;                  // ring stages per warp
+constexpr size_t kW4SmemCap = 226 * 1024;
+constexpr size_t kW4OutCap = 32 * 1024;       // sums of a slab
+constexpr int kW4MaxCluster = 8;
+
+// MMA column tiles of a pass and its tokens. An activation is three 8-bit
+// digits, each in an MMA column of its own. With one or two tiles the columns
+// are packed (token c/3, digit c mod 3); otherwise three tiles take the three
+// digits of eight tokens, so that a lane holds a token's digits itself.
+template <int NT>
+struct W4Pass {
+  static constexpr bool kPlanar = NT >= 3;
+  static constexpr int kTok = kPlanar ? 8 * (NT / 3) : 8 * NT / 3;
+  static constexpr int kSums = kPlanar ? 8 * (NT / 3) : 8 * NT;  // sums per weight row
+  static constexpr int kCols = 8 * NT;
+};
+
+// Shared memory of a CTA, in bytes from its start.
+struct W4Smem {
+  uint32_t part;   // float [warp][2][16][sums]: a run's first and last shares
+  uint32_t ring;   // [warp][stage]: codes, scales, zero points
+  uint32_t out;    // float [row block][token][16]
+  uint32_t dsum;   // int [group][column]: digit sums
+  uint32_t cf;     // float [block][column]: what a digit counts
+  uint32_t x;      // digits, [column][x_stride]
+  uint32_t x_stride, total;
+};
+template <int V>
+__host__ __device__ constexpr int w4_stage_bytes() {
+  return 1024 + 48 * V;
+}
+// KB: blocks of K of this CTA, at most; slab: row blocks, at most.
+template <int V, int NT>
+__host__ __device__ inline W4Smem w4_smem(int KB, int slab, int toks, int stages) {
+  using C = W4Pass<NT>;
+  W4Smem s;
+  s.part = 0;
+  s.ring = s.part + 2 * kW4Warps * 16 * C::kSums * 4;
+  s.out = s.ring + kW4Warps * stages * w4_stage_bytes<V>();
+  s.dsum = s.out + slab * toks * 64;
+  s.cf = s.dsum + KB * V * C::kCols * 4;
+  s.x = s.cf + KB * C::kCols * 4;
+  // 16 bytes more than the row: two columns (the eight lanes of a 16-byte
+  // read) then fall on different banks
+  s.x_stride = KB * 128 + 16;
+  s.total = s.x + 3 * toks * s.x_stride;
+  return s;
+}
+
+// The warp whose run holds item i of `items` (runs as in the kernel).
+__device__ __forceinline__ int w4_warp_of(int i, int items) {
+  int w = (int)(((int64_t)i * kW4Warps) / items);
+  while (w + 1 < kW4Warps && (int)((int64_t)items * (w + 1) / kW4Warps) <= i) ++w;
+  return w;
+}
+
+// Sum of token c, row r of a row block over the shares of warps w_lo..w_hi (the
+// first in `slot_lo`, the others in their slot 0), lowest digit first.
+template <int NT>
+__device__ __forceinline__ float w4_gather(const float* part, int w_lo, int w_hi, int slot_lo, int r,
+                                           int c) {
+  constexpr int SUMS = W4Pass<NT>::kSums, P = W4Pass<NT>::kPlanar ? 1 : 3;
+  float y = 0.f;
+#pragma unroll
+  for (int pc = P - 1; pc >= 0; --pc) {
+    y += part[(slot_lo * 16 + r) * SUMS + c * P + pc];
+    for (int w = w_lo + 1; w <= w_hi; ++w) y += part[(w * 32 + r) * SUMS + c * P + pc];
+  }
+  return y;
+}
+
+// Activations of one CTA's K blocks into shared memory, as digits. Per token
+// and 128-column block: the largest power of two f with max|x|·f ≤ 127·2^16, then
+// x·f rounded to a 24-bit integer d2·2^16 + d1·2^8 + d0 with digits in
+// [−128, 127] (adding 0x808080 and flipping the same bits carries between
+// them), and what digit i counts, 2^(8i)/f. Sixteen lanes take a block, eight
+// columns each. The rounding, half of 1/f, is at most 2^-23 of the block's
+// largest value: what aligning to it in an fp32 sum would lose.
+template <typename T, int V, int NT>
+__device__ __forceinline__ void w4_stage_x(uint8_t* smem, const W4Smem& L, const T* X, int64_t K,
+                                           int kb0, int KB, int toks) {
+  constexpr bool PL = W4Pass<NT>::kPlanar;
+  constexpr int COLS = W4Pass<NT>::kCols, B = 4, GL = 16 / V;  // GL lanes per group
+  const int units = KB * 16, total = units * toks;
+  const int l = threadIdx.x & 15;
+  for (int i0 = threadIdx.x & ~15; i0 < total; i0 += B * kW4Threads) {
+    float v[B][8];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {  // the loads of a few blocks in flight together
+      const int i = i0 + b * kW4Threads + l, m = i / units, u = i - m * units;
+      const int64_t k = ((int64_t)kb0 * 16 + u) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[b][j] = 0.f;
+      if (i < total && k < K) {
+        const T* p = X + (int64_t)m * K + k;
+        if constexpr (sizeof(T) == 2) {
+          const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[b][2 * j] = __uint_as_float(w[j] << 16);
+            v[b][2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+          }
+        } else {
+          const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+          const float4 c = __ldg(reinterpret_cast<const float4*>(p) + 1);
+          v[b][0] = a.x; v[b][1] = a.y; v[b][2] = a.z; v[b][3] = a.w;
+          v[b][4] = c.x; v[b][5] = c.y; v[b][6] = c.z; v[b][7] = c.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int i = i0 + b * kW4Threads;  // the block's first unit
+      if (i >= total) break;              // the same for its sixteen lanes
+      const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
+      const int m = i / units, u = i - m * units, kb = u >> 4;
+      uint32_t top = 0;  // largest magnitude, as bits: an infinity or NaN stays on top
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[b][j]) & 0x7FFFFFFFu);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+      // f = 2^e, at most 2^125: a block below 1e-31 keeps fewer bits
+      const float f0 = __fdiv_rn(8323072.0f, fmaxf(__uint_as_float(top), 1e-31f));
+      const float f = __uint_as_float(__float_as_uint(f0) & 0xFF800000u);
+      // an infinity or NaN makes the token's results NaN
+      const float unit = top < 0x7F800000u ? __fdiv_rn(1.0f, f) : __uint_as_float(0x7FFFFFFFu);
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        w[j] = ((uint32_t)__float2int_rn(__fmul_rn(v[b][j], f)) + 0x808080u) ^ 0x808080u;
+      uint32_t lane_off = kb * 128 + (l & 3) * 32 + (l >> 2) * 8;  // [t][u][8 bytes]
+#pragma unroll
+      for (int d = 0; d < 3; ++d) {  // digit d: byte d of the eight words
+        const uint32_t sel = d | ((4 + d) << 4);
+        const uint32_t a04 = __byte_perm(w[0], w[4], sel), a15 = __byte_perm(w[1], w[5], sel);
+        const uint32_t a26 = __byte_perm(w[2], w[6], sel), a37 = __byte_perm(w[3], w[7], sel);
+        const uint32_t b0 = __byte_perm(a04, a15, 0x5410), b1 = __byte_perm(a26, a37, 0x5410);
+        // columns of the MMA: digit d of token m
+        const int pc = 2 - d;  // the highest digit first
+        const int xc = m * 3 + pc;
+        const int col = PL ? (m >> 3) * 24 + pc * 8 + (m & 7) : xc;
+        *reinterpret_cast<uint2*>(smem + L.x + xc * L.x_stride + lane_off) = make_uint2(b0, b1);
+        int s = dp4a(b1, 0x01010101u, dp4a(b0, 0x01010101u, 0));
+#pragma unroll
+        for (int o = 1; o < GL; o <<= 1) s += __shfl_xor_sync(mask, s, o);
+        if (l % GL == 0)
+          reinterpret_cast<int*>(smem + L.dsum)[(kb * V + l / GL) * COLS + col] = s;
+        if (l == d)
+          reinterpret_cast<float*>(smem + L.cf)[kb * COLS + col] =
+              __fmul_rn(unit, d == 2 ? 65536.0f : (d == 1 ? 256.0f : 1.0f));
+      }
+    }
+  }
+}
+
+// Y = X·Wᵀ for up to W4Pass<NT>::kTok tokens per grid row.
+//
+// Legacy bf16 MMAs run at an eighth of the int8 ones here (m16n8k16 takes 32
+// cycles of a sub-partition's tensor pipe, m16n8k32 of int8 under 9), so the
+// product is one of integers: the codes as bytes against the activations'
+// digits, Σ q·d − z·Σ d exact in int32 for a group, then one fp32
+// multiply-add per group with s times what the digit counts.
+//
+// Each CTA owns a slab of 16-row blocks, contiguous in memory; its 16 warps
+// take equal, contiguous runs of the slab's 1 KB blocks, so the load is even
+// whatever the shape. The sums of a row block that a run holds whole are
+// complete; the first and the last, which it may share with its neighbours,
+// meet in shared memory at the end, in the order of the warps. The CTAs of a
+// cluster share a slab: each takes a range of K, so that its activations fit
+// in shared memory, and the slab's sums meet there, in the order of the CTAs.
+template <typename T, int V, int NT>
+__global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Params p) {
+  using C = W4Pass<NT>;
+  constexpr int SUMS = C::kSums, COLS = C::kCols, TOK = C::kTok, ST = w4_stage_bytes<V>();
+  constexpr int NA = SUMS / 8;                  // accumulator tiles
   extern __shared__ __align__(16) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int S = p.split, D = p.depth, G = kW4Warps / S;
-  const int group = warp / S, ks = warp - group * S;
-  float* part = reinterpret_cast<float*>(smem);
-  uint8_t* ring = smem + w4_part_bytes<NT>() + warp * (D * ST);
-  uint8_t* xs = smem + w4_fixed_bytes<V, NT>(D);
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int D = p.stages, ranks = (int)cluster_size(), rank = (int)cluster_rank();
   // Blocks are counted in 32 bits: 2^31 of them are 2 TB.
-  const int RB = (int)((p.N + 15) / 16), KB = (int)((p.K + 127) / 128);
-  const int rb0 = (int)((int64_t)RB * blockIdx.x / gridDim.x);
-  const int rb1 = (int)((int64_t)RB * (blockIdx.x + 1) / gridDim.x);
+  const int RB = (int)((p.N + 15) / 16), KBt = (int)((p.K + 127) / 128);
+  const int slab = (int)blockIdx.x / ranks;
+  const int rb0 = (int)((int64_t)RB * slab / p.slabs), rb1 = (int)((int64_t)RB * (slab + 1) / p.slabs);
+  const int kb0 = KBt * rank / ranks, KB = KBt * (rank + 1) / ranks - kb0;
+  const int nrb = rb1 - rb0, items = nrb * KB;
+  const int it0 = (int)((int64_t)items * warp / kW4Warps);
+  const int it1 = (int)((int64_t)items * (warp + 1) / kW4Warps);
   const int64_t m0 = (int64_t)blockIdx.y * TOK;
-  const int toks = (int)min((int64_t)TOK, p.M - m0), cols = toks * P;
-  const T* X = reinterpret_cast<const T*>(p.X) + m0 * p.K;
-  const int xstride = (int)w4_x_stride(p.K);
+  const int toks = (int)min((int64_t)TOK, p.M - m0);
+  const W4Smem L = w4_smem<V, NT>((KBt + ranks - 1) / ranks, (RB + p.slabs - 1) / p.slabs,
+                                  (int)min((int64_t)TOK, p.M), D);
+  float* part = reinterpret_cast<float*>(smem + L.part);
+  float* out = reinterpret_cast<float*>(smem + L.out);
 
   pdl_launch_dependents();
-  // Requests run ahead of the compute loop over the same blocks: 1024 bytes of
-  // codes, two pieces per lane, and 32·V bytes of scales and 16·V of zero
-  // points by the first lanes. The first ones go out before the wait for the
-  // previous kernel, which does not write the weights.
-  const uint8_t* w_src = p.W4 + 16 * lane;
+  // Requests run ahead of the compute loop: 1024 bytes of codes, two pieces
+  // per lane, and 32·V bytes of scales and 16·V of zero points by the first
+  // lanes. The first ones go out before the wait for the previous kernel,
+  // which does not write the weights.
   const bool is_scale = lane < 2 * V, has_aux = is_scale || (lane < 3 * V && p.zeros != nullptr);
-  const uint8_t* aux_src = is_scale ? reinterpret_cast<const uint8_t*>(p.scales) + 16 * lane
-                                    : p.zeros + 16 * (lane - 2 * V);
   const uint32_t aux_step = is_scale ? 32 * V : 16 * V;
-  const uint32_t ring_s = smem_u32(ring), ring_end = ring_s + D * ST;
-  uint32_t q_dst = ring_s + 16 * lane;
-  int q_rb = ks < KB ? rb0 + group : rb1, q_kb = ks;
+  int q_kb = KB > 0 ? it0 % KB : 0;
+  const int64_t first = (int64_t)(rb0 + (KB > 0 ? it0 / KB : 0)) * KBt + kb0 + q_kb;
+  const uint8_t* w_src = p.W4 + first * 1024 + 16 * lane;
+  const uint8_t* aux_src = (is_scale ? reinterpret_cast<const uint8_t*>(p.scales) + 16 * lane
+                                     : p.zeros + 16 * (lane - 2 * V)) +
+                           first * aux_step;
+  const uint32_t ring = smem_u32(smem) + L.ring + warp * (D * ST), ring_end = ring + D * ST;
+  uint32_t q_dst = ring;
+  int left = it1 - it0;
   auto request = [&]() {
-    if (q_rb < rb1) {
-      const uint32_t blk = (uint32_t)q_rb * KB + q_kb;
-      const uint8_t* w = w_src + (uint64_t)blk * 1024u;
-      cp_async16(q_dst, w);
-      cp_async16(q_dst + 512, w + 512);
-      if (has_aux) cp_async16(q_dst + 1024, aux_src + (uint64_t)blk * aux_step);
-      q_kb += S;
-      if (q_kb >= KB) {
-        q_kb = ks;
-        q_rb += G;
+    if (left > 0) {
+      cp_async16(q_dst + 16 * lane, w_src);
+      cp_async16(q_dst + 16 * lane + 512, w_src + 512);
+      if (has_aux) cp_async16(q_dst + 16 * lane + 1024, aux_src);
+      int step = 1;
+      if (++q_kb == KB) {  // on to the next row block, past the other CTAs' blocks
+        q_kb = 0;
+        step += KBt - KB;
       }
+      w_src += step * 1024;
+      aux_src += step * aux_step;
       q_dst += ST;
-      if (q_dst >= ring_end) q_dst -= D * ST;
+      if (q_dst == ring_end) q_dst = ring;
+      --left;
     }
     cp_async_commit();
   };
   for (int d = 0; d < D - 1; ++d) request();
   pdl_wait_prior_grid();
 
-  if constexpr (XS) {
-    const int units = KB * 16;  // 8 columns of K each
-    constexpr int B = P == 1 ? 4 : 2;
-    for (int c = 0; c < toks; c += B) {  // a few tokens' loads in flight together
-      for (int u = tid; u < units; u += kW4Threads) {
-        W4Eight<T> e[B];
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-          e[b].clear();
-          if (c + b < toks && 8 * u < p.K) e[b].load(X + (int64_t)(c + b) * p.K + 8 * u);
-        }
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-          if (c + b < toks) {
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-              *reinterpret_cast<uint4*>(xs + ((c + b) * P + i) * xstride + 16 * u) = e[b].piece();
-          }
-        }
-      }
-    }
-    __syncthreads();
-  }
+  w4_stage_x<T, V, NT>(smem, L, reinterpret_cast<const T*>(p.X) + m0 * p.K, p.K, kb0, KB, toks);
+  if (it0 == it1)  // fewer blocks than warps: an empty run adds nothing
+    for (int j = lane; j < 16 * SUMS; j += 32) part[warp * 32 * SUMS + j] = 0.f;
+  __syncthreads();
 
-  // Activations of the lane's MMA columns 8n + g; columns past the tokens stay 0.
+  // Digits of the lane's MMA columns 8n + g. Columns past the tokens repeat
+  // another's: what they sum to is never read.
   uint32_t xaddr[NT];
-  bool live[NT];
-  uint4 x[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    live[n] = 8 * n + g < cols;
-    xaddr[n] = smem_u32(xs + (8 * n + g) * xstride + 16 * t);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) x[n][u] = make_uint4(0u, 0u, 0u, 0u);
+    int xc;
+    if constexpr (C::kPlanar)
+      xc = (8 * (n / 3) + g) % toks * 3 + n % 3;
+    else
+      xc = (8 * n + g) % (3 * toks);
+    xaddr[n] = smem_u32(smem) + L.x + xc * L.x_stride + 32 * t;
   }
+  const uint32_t dsum = smem_u32(smem) + L.dsum + 8 * t, cf = smem_u32(smem) + L.cf + 8 * t;
 
-  const uint32_t ones = p.ones;
-  uint32_t src = ring_s;
-  int buf = 0;
-  for (int rb = rb0 + group; rb < rb1; rb += G) {
-    float acc[NT][4];
+  uint32_t src = ring;
+  int rb = KB > 0 ? it0 / KB : 0, kb = it0 - rb * KB, slot = 0;
+  for (int it = it0; it < it1;) {
+    const int begin = kb, end = min(KB, kb + (it1 - it));  // this run's part of row block rb
+    float acc[NA][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-    for (int kb = ks; kb < KB; kb += S) {
-      __syncwarp();  // the stage read last is free: every lane is past its reads
-      request();
-      if (D == 8)
-        cp_async_wait<7>();
-      else if (D == 4)
-        cp_async_wait<3>();
-      else
+    for (int n = 0; n < NA; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+    for (; kb < end; ++kb) {
+      // D − 1 blocks are under way; the oldest is next. Past the barrier every
+      // lane sees it and is done with the stage before it, which is filled anew.
+      if (D == 4)
+        cp_async_wait<2>();
+      else if (D == 3)
         cp_async_wait<1>();
+      else
+        cp_async_wait<0>();
       __syncwarp();
-      const uint4 wlo = lds128(src + 16 * lane), whi = lds128(src + 512 + 16 * lane);
+      request();
+      const uint4 wlo = lds128(src + 16 * lane), whi = lds128(src + 16 * lane + 512);
       const uint32_t lo[4] = {wlo.x, wlo.y, wlo.z, wlo.w}, hi[4] = {whi.x, whi.y, whi.z, whi.w};
+      uint32_t a[4][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if constexpr (XS) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) lds128_if(x[n][u], xaddr[n] + kb * 256 + 64 * u, live[n]);
-        } else {
-          const int c = 8 * n + g;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int64_t k = (int64_t)kb * 128 + 32 * u + 8 * t;
-            W4Eight<T> e;
-            e.clear();
-            if (live[n] && k < p.K) e.load(X + (int64_t)(c / P) * p.K + k);
-            x[n][u] = e.piece();
-            for (int i = 0; i < c % P; ++i) x[n][u] = e.piece();
-          }
-        }
+      for (int u = 0; u < 4; ++u) {
+        a[u][0] = lo[u] & 0x0F0F0F0Fu;
+        a[u][1] = hi[u] & 0x0F0F0F0Fu;
+        a[u][2] = (lo[u] >> 4) & 0x0F0F0F0Fu;
+        a[u][3] = (hi[u] >> 4) & 0x0F0F0F0Fu;
       }
-      float pa[NT][4];
+      float s0[V], s1[V];
+      int z0[V], z1[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        // bf16 1 + z/128 twice, for rows g and g + 8: z in the mantissa
-        uint32_t z = 0x0808u;
-        if (p.zeros != nullptr) z = lds_u16(src + 1024 + 32 * V + (g * V + v) * 2);
-        z |= 0x3F8080u;
-        const uint32_t z0 = __byte_perm(z, 0u, 0x2020), z1 = __byte_perm(z, 0u, 0x2121);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) pa[n][0] = pa[n][1] = pa[n][2] = pa[n][3] = 0.f;
-#pragma unroll
-        for (int u = v * (4 / V); u < (v + 1) * (4 / V); ++u) {
-          uint32_t a[8];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            a[2 * q] = w4_pair(lo[u], q, ones, z0);
-            a[2 * q + 1] = w4_pair(hi[u], q, ones, z1);
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_bf16_16816(pa[n], a[0], a[1], a[2], a[3], x[n][u].x, x[n][u].y);
-            mma_bf16_16816(pa[n], a[4], a[5], a[6], a[7], x[n][u].z, x[n][u].w);
-          }
-        }
         const uint32_t s = lds_u32(src + 1024 + (g * V + v) * 4);
-        const float s0 = __uint_as_float(s << 16), s1 = __uint_as_float(s & 0xFFFF0000u);
+        s0[v] = __uint_as_float(s << 16);
+        s1[v] = __uint_as_float(s & 0xFFFF0000u);
+        const uint32_t z = p.zeros != nullptr ? lds_u16(src + 1024 + 32 * V + (g * V + v) * 2) : 0x0808u;
+        z0[v] = -(int)(z & 0xFFu);
+        z1[v] = -(int)(z >> 8);
+      }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          acc[n][0] = fmaf(s0, pa[n][0], acc[n][0]);
-          acc[n][1] = fmaf(s0, pa[n][1], acc[n][1]);
-          acc[n][2] = fmaf(s1, pa[n][2], acc[n][2]);
-          acc[n][3] = fmaf(s1, pa[n][3], acc[n][3]);
+      for (int n = 0; n < NA; ++n) {
+        constexpr int ND = C::kPlanar ? 3 : 1;  // tiles of this accumulator: digits, or one
+        int d[ND][V][4];
+        float f[ND][2];
+#pragma unroll
+        for (int j = 0; j < ND; ++j) {
+          const int tile = n * ND + j;
+          const uint4 x0 = lds128(xaddr[tile] + kb * 128), x1 = lds128(xaddr[tile] + kb * 128 + 16);
+          const uint32_t b[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            // −z·Σd on top of the bits of 1.5·2^23: after the MMAs the float with
+            // these bits, less 1.5·2^23, is the sum (|sum| < 2^19)
+            const uint32_t o = dsum + ((kb * V + v) * COLS + 8 * tile) * 4;
+            const int ds0 = (int)lds_u32(o), ds1 = (int)lds_u32(o + 4);
+            d[j][v][0] = ds0 * z0[v] + 0x4B400000;
+            d[j][v][1] = ds1 * z0[v] + 0x4B400000;
+            d[j][v][2] = ds0 * z1[v] + 0x4B400000;
+            d[j][v][3] = ds1 * z1[v] + 0x4B400000;
+#pragma unroll
+            for (int u = v * (4 / V); u < (v + 1) * (4 / V); ++u)
+              mma_u8s8_16832(d[j][v], a[u][0], a[u][1], a[u][2], a[u][3], b[2 * u], b[2 * u + 1]);
+          }
+          f[j][0] = __uint_as_float(lds_u32(cf + (kb * COLS + 8 * tile) * 4));
+          f[j][1] = __uint_as_float(lds_u32(cf + (kb * COLS + 8 * tile) * 4 + 4));
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+          for (int j = ND - 1; j >= 0; --j) {
+            acc[n][0] = fmaf(__int_as_float(d[j][v][0]) - 12582912.0f, s0[v] * f[j][0], acc[n][0]);
+            acc[n][1] = fmaf(__int_as_float(d[j][v][1]) - 12582912.0f, s0[v] * f[j][1], acc[n][1]);
+            acc[n][2] = fmaf(__int_as_float(d[j][v][2]) - 12582912.0f, s1[v] * f[j][0], acc[n][2]);
+            acc[n][3] = fmaf(__int_as_float(d[j][v][3]) - 12582912.0f, s1[v] * f[j][1], acc[n][3]);
+          }
         }
       }
       src += ST;
-      if (src >= ring_end) src -= D * ST;
+      if (src == ring_end) src = ring;
     }
-    // The group's sums of this row block. Two buffers: a warp overwrites one
-    // only after the barrier of the row block between, when every warp of the
-    // group has read it.
-    float* mine = part + ((buf * kW4Warps + warp) * 16 + g) * COLS + 2 * t;
+    it += end - begin;
+    // The share of row block rb: slot 0 for the run's first, 1 for a later one.
+    float* mine = part + ((warp * 2 + slot) * 16 + g) * SUMS + 2 * t;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NA; ++n) {
       *reinterpret_cast<float2*>(mine + 8 * n) = make_float2(acc[n][0], acc[n][1]);
-      *reinterpret_cast<float2*>(mine + 8 * n + 8 * COLS) = make_float2(acc[n][2], acc[n][3]);
+      *reinterpret_cast<float2*>(mine + 8 * n + 8 * SUMS) = make_float2(acc[n][2], acc[n][3]);
     }
-    if (S == 1)
+    if (begin == 0 && end == KB) {  // whole
       __syncwarp();
-    else
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * S) : "memory");
-    const float* sums = part + (buf * kW4Warps + group * S) * 16 * COLS;
-    for (int j = ks * 32 + lane; j < 16 * toks; j += 32 * S) {
-      const int r = j & 15, c = j >> 4;
-      float y = 0.f;
-#pragma unroll
-      for (int pc = P - 1; pc >= 0; --pc)
-        for (int w = 0; w < S; ++w) y += sums[(w * 16 + r) * COLS + c * P + pc];
-      y *= kW4Unit;
-      const int64_t row = (int64_t)rb * 16 + r, o = (m0 + c) * p.N + row;
-      if (row < p.N) {
-        if (p.y_bf16)
-          reinterpret_cast<__nv_bfloat16*>(p.Y)[o] = __float2bfloat16_rn(y);
-        else
-          reinterpret_cast<float*>(p.Y)[o] = y;
-      }
+      for (int j = lane; j < 16 * toks; j += 32)
+        out[rb * toks * 16 + j] = w4_gather<NT>(part, warp, warp, warp * 2 + slot, j & 15, j >> 4);
+      __syncwarp();
+    } else {
+      slot = 1;
     }
-    if (S == 1) __syncwarp();
-    buf ^= 1;
+    kb = 0;
+    ++rb;
   }
+  __syncthreads();
+  // Row blocks that several runs share.
+  for (int j = tid; j < nrb * 16 * toks; j += kW4Threads) {
+    const int r = j / (16 * toks);
+    if (KB == 0) {
+      out[j] = 0.f;
+      continue;
+    }
+    const int w_lo = w4_warp_of(r * KB, items), w_hi = w4_warp_of(r * KB + KB - 1, items);
+    if (w_lo == w_hi) continue;
+    // the first of them may have begun in an earlier row block
+    const int started = (int)((int64_t)items * w_lo / kW4Warps);
+    const int i = j - r * 16 * toks;
+    out[j] = w4_gather<NT>(part, w_lo, w_hi, w_lo * 2 + (started < r * KB ? 1 : 0), i & 15, i >> 4);
+  }
+  __syncwarp();
+  if (ranks > 1)
+    cluster_barrier();
+  else
+    __syncthreads();
+  const int rows = nrb * 16;
+  for (int j = tid + rank * kW4Threads; j < rows * toks; j += kW4Threads * ranks) {
+    const int c = j / rows, r = j - c * rows, o = ((r >> 4) * toks + c) * 16 + (r & 15);
+    float y = 0.f;
+    if (ranks > 1) {
+      for (int k = 0; k < ranks; ++k) y += cluster_lds_f32(smem_u32(out + o), k);
+    } else {
+      y = out[o];
+    }
+    const int64_t row = (int64_t)rb0 * 16 + r, at = (m0 + c) * p.N + row;
+    if (row < p.N) {
+      if (p.y_bf16)
+        reinterpret_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(y);
+      else
+        reinterpret_cast<float*>(p.Y)[at] = y;
+    }
+  }
+  __syncwarp();
+  if (ranks > 1) cluster_barrier();  // the others may still read this CTA's sums
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // ---------------------------------------------------------------------------

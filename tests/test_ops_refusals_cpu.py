@@ -56,6 +56,8 @@ def test_w4_refusals(lib, p):
     assert f(p, 1, 1, 64, p, p, None, 16, 96, p, 1, 0, None) == BAD_SHAPE
     assert f(p, 1, 1, 96, p, p, None, 16, 32, p, 1, 0, None) == BAD_SHAPE
     assert f(p, 1, 1, (1 << 22) + 64, p, p, None, 16, 32, p, 1, 0, None) == BAD_SHAPE
+    assert f(p, 1, 1, 262144 + 64, p, p, None, 16, 32, p, 1, 0, None) == BAD_SHAPE
+    assert f(None, 1, 0, 262144, None, None, None, 16, 32, None, 1, 0, None) == 0
     assert f(p, 1, -1, 64, p, p, None, 16, 32, p, 1, 0, None) == BAD_SHAPE
     assert f(p, 2, 1, 64, p, p, None, 16, 32, p, 1, 0, None) == BAD_DTYPE
     assert f(p, 1, 1, 64, p, p, None, 16, 32, p, 1, 2, None) == BAD_ARG    # BL_FLAG_RAW_I32
