@@ -858,9 +858,6 @@ inline unsigned loop_grid(int64_t items, int64_t per, int sms) {
   return (unsigned)(b < 1 ? 1 : b);
 }
 
-#ifndef W4CTAS
-#define W4CTAS 2
-#endif
 // One launch: slabs × clusters. Returns BL_ERR_SHAPE where the activations of
 // a pass do not fit.
 template <typename T, int V, int NT>
@@ -868,36 +865,27 @@ bl_status launch_w4_nt(W4Params p, bool pdl, int dev, int sms, cudaStream_t st) 
   using C = W4Pass<NT>;
   const int64_t RB = (p.N + 15) / 16, KB = (p.K + 127) / 128;
   const int toks = (int)(p.M < C::kTok ? p.M : C::kTok);
-  // The smallest cluster, and the most ring stages with it, that fit.
-  const int64_t out_rows = (int64_t)(kW4OutCap / (64 * toks));
-  int ranks = 1, stages = 0;
+  // The smallest cluster that fits, one CTA per SM. Clusters keep their slab's
+  // sums in shared memory, at most kW4OutCap bytes of them.
+  int ranks = 1;
   size_t smem = 0;
   int64_t slabs = 0;
-  for (; ranks <= kW4MaxCluster && stages == 0; ranks *= 2) {
-    const int64_t kb = (KB + ranks - 1) / ranks;
-    for (int s = kW4Stages; s >= (ranks < kW4MaxCluster ? 3 : 2); --s) {
-      // two CTAs per SM where two fit, as many slabs as there is room for them
-      for (int per_sm = NT == 1 ? W4CTAS : 1; per_sm >= 1; --per_sm) {
-        int64_t n = (int64_t)per_sm * sms / ranks;
-        if (n > RB) n = RB;
-        if (n * out_rows < RB) n = (RB + out_rows - 1) / out_rows;
-        if (3 * toks * kb * 128 > (int64_t)kW4SmemCap) continue;
-        const size_t need = w4_smem<V, NT>((int)kb, (int)((RB + n - 1) / n), toks, s).total;
-        if (need > (per_sm == 2 ? 113 * 1024 : kW4SmemCap)) continue;
-        stages = s;
-        smem = need;
-        slabs = n;
-        break;
-      }
-      if (stages != 0) break;
-    }
-    if (stages != 0) break;
+  for (; ranks <= kW4MaxCluster; ranks *= 2) {
+    const int64_t kb = (KB + ranks - 1) / ranks, out_rows = (int64_t)(kW4OutCap / (64 * toks));
+    if (3 * toks * kb * 128 > (int64_t)kW4SmemCap) continue;
+    int64_t n = sms / ranks;
+    if (n > RB) n = RB;
+    if (ranks > 1 && n * out_rows < RB) n = (RB + out_rows - 1) / out_rows;
+    smem = w4_smem<V, NT>((int)kb, (int)((RB + n - 1) / n), toks, ranks).total;
+    if (smem > kW4SmemCap) continue;
+    slabs = n;
+    break;
   }
-  if (stages == 0) return BL_ERR_SHAPE;
+  if (slabs == 0) return BL_ERR_SHAPE;
   auto* k = w4_linear_kernel<T, V, NT>;
   BL_TRY(ensure_smem(k, dev, smem));
-  p.stages = stages;
-  p.slabs = (int)slabs;
+  p.slab_rows = (int)(RB / slabs);
+  p.slab_more = (int)(RB % slabs);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(slabs * ranks), (unsigned)((p.M + C::kTok - 1) / C::kTok));
   cfg.blockDim = dim3(kW4Threads);

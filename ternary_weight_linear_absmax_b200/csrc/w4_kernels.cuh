@@ -30,23 +30,19 @@ struct W4Params {
   void* Y;                        // [M, N] fp32/bf16
   int64_t M, N, K;
   int y_bf16;
-  int stages;                     // ring stages per warp: 2, 3 or 4
-  int slabs;                      // slabs of row blocks (grid.x = slabs × CTAs per cluster)
+  int slab_rows, slab_more;       // row blocks per slab; the first slab_more have one more
 };
 
+// d = A·B + c.
 __device__ __forceinline__ void mma_u8s8_16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+                                               uint32_t a3, uint32_t b0, uint32_t b1, const int (&c)[4]) {
   asm volatile(
       "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -55,6 +51,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
@@ -91,7 +92,6 @@ __device__ __forceinline__ float cluster_lds_f32(uint32_t addr, uint32_t rank) {
 
 constexpr int kW4Warps = 16;
 constexpr int kW4Threads = 32 * kW4Warps;
-constexpr int kW4Stages = 4;                  // ring stages per warp
 constexpr size_t kW4SmemCap = 226 * 1024;
 constexpr size_t kW4OutCap = 32 * 1024;       // sums of a slab
 constexpr int kW4MaxCluster = 8;
@@ -105,16 +105,15 @@ struct W4Pass {
   static constexpr bool kPlanar = NT >= 3;
   static constexpr int kTok = kPlanar ? 8 * (NT / 3) : 8 * NT / 3;
   static constexpr int kSums = kPlanar ? 8 * (NT / 3) : 8 * NT;  // sums per weight row
-  static constexpr int kCols = 8 * NT;
 };
 
 // Shared memory of a CTA, in bytes from its start.
 struct W4Smem {
   uint32_t part;   // float [warp][2][16][sums]: a run's first and last shares
   uint32_t ring;   // [warp][stage]: codes, scales, zero points
-  uint32_t out;    // float [row block][token][16]
-  uint32_t dsum;   // int [group][column]: digit sums
-  uint32_t cf;     // float [block][column]: what a digit counts
+  uint32_t out;    // float [row block][token][16], in a cluster
+  uint32_t dsum;   // float [group][sum]: the activations' sums, in fixed point
+  uint32_t cf;     // float [block][sum]: what a digit, or 1 in fixed point, counts
   uint32_t x;      // digits, [column][x_stride]
   uint32_t x_stride, total;
 };
@@ -122,17 +121,23 @@ template <int V>
 __host__ __device__ constexpr int w4_stage_bytes() {
   return 1024 + 48 * V;
 }
+// Ring stages per warp: three where the scales make a stage longer, so that the
+// longest rows fit for every group size.
+template <int V>
+__host__ __device__ constexpr int w4_stages() {
+  return V == 4 ? 3 : 4;
+}
 // KB: blocks of K of this CTA, at most; slab: row blocks, at most.
 template <int V, int NT>
-__host__ __device__ inline W4Smem w4_smem(int KB, int slab, int toks, int stages) {
+__host__ __device__ inline W4Smem w4_smem(int KB, int slab, int toks, int ranks) {
   using C = W4Pass<NT>;
   W4Smem s;
   s.part = 0;
   s.ring = s.part + 2 * kW4Warps * 16 * C::kSums * 4;
-  s.out = s.ring + kW4Warps * stages * w4_stage_bytes<V>();
-  s.dsum = s.out + slab * toks * 64;
-  s.cf = s.dsum + KB * V * C::kCols * 4;
-  s.x = s.cf + KB * C::kCols * 4;
+  s.out = s.ring + kW4Warps * w4_stages<V>() * w4_stage_bytes<V>();
+  s.dsum = s.out + (ranks > 1 ? slab * toks * 64 : 0);
+  s.cf = s.dsum + KB * V * C::kSums * 4;
+  s.x = s.cf + KB * C::kSums * 4;
   // 16 bytes more than the row: two columns (the eight lanes of a 16-byte
   // read) then fall on different banks
   s.x_stride = KB * 128 + 16;
@@ -140,10 +145,26 @@ __host__ __device__ inline W4Smem w4_smem(int KB, int slab, int toks, int stages
   return s;
 }
 
+// One warp's request of a block into a ring stage: two 16-byte pieces of codes
+// per lane, one of scales or zero points where `aux`; nothing with `left` ≤ 0.
+__device__ __forceinline__ void w4_request(uint32_t dst, const uint8_t* w, const uint8_t* aux, int left,
+                                           int has_aux) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.gt.s32 p, %3, 0;\n\t"
+      "setp.ne.and.s32 q, %4, 0, p;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t"
+      "@p cp.async.cg.shared.global [%0 + 512], [%1 + 512], 16;\n\t"
+      "@q cp.async.cg.shared.global [%0 + 1024], [%2], 16;\n\t"
+      "cp.async.commit_group;\n\t}" ::"r"(dst),
+      "l"(w), "l"(aux), "r"(left), "r"(has_aux)
+      : "memory");
+}
+
 // The warp whose run holds item i of `items` (runs as in the kernel).
 __device__ __forceinline__ int w4_warp_of(int i, int items) {
-  int w = (int)(((int64_t)i * kW4Warps) / items);
-  while (w + 1 < kW4Warps && (int)((int64_t)items * (w + 1) / kW4Warps) <= i) ++w;
+  int w = i * kW4Warps / items;
+  while (w + 1 < kW4Warps && items * (w + 1) / kW4Warps <= i) ++w;
   return w;
 }
 
@@ -162,6 +183,17 @@ __device__ __forceinline__ float w4_gather(const float* part, int w_lo, int w_hi
   return y;
 }
 
+// Output j of a row block: row j mod 16 of token j/16 of the pass.
+__device__ __forceinline__ void w4_store(const W4Params& p, int rb, int64_t m0, int j, float y) {
+  const int64_t row = (int64_t)rb * 16 + (j & 15), at = (m0 + (j >> 4)) * p.N + row;
+  if (row < p.N) {
+    if (p.y_bf16)
+      reinterpret_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(y);
+    else
+      reinterpret_cast<float*>(p.Y)[at] = y;
+  }
+}
+
 // Activations of one CTA's K blocks into shared memory, as digits. Per token
 // and 128-column block: the largest power of two f with max|x|·f ≤ 127·2^16, then
 // x·f rounded to a 24-bit integer d2·2^16 + d1·2^8 + d0 with digits in
@@ -169,23 +201,28 @@ __device__ __forceinline__ float w4_gather(const float* part, int w_lo, int w_hi
 // them), and what digit i counts, 2^(8i)/f. Sixteen lanes take a block, eight
 // columns each. The rounding, half of 1/f, is at most 2^-23 of the block's
 // largest value: what aligning to it in an fp32 sum would lose.
-template <typename T, int V, int NT>
+template <typename T, int V, int NT, int B>
 __device__ __forceinline__ void w4_stage_x(uint8_t* smem, const W4Smem& L, const T* X, int64_t K,
                                            int kb0, int KB, int toks) {
   constexpr bool PL = W4Pass<NT>::kPlanar;
-  constexpr int COLS = W4Pass<NT>::kCols, B = 4, GL = 16 / V;  // GL lanes per group
+  constexpr int SUMS = W4Pass<NT>::kSums, GL = 16 / V;  // GL lanes per group
+  float* dsum = reinterpret_cast<float*>(smem + L.dsum);
+  float* cf = reinterpret_cast<float*>(smem + L.cf);
   const int units = KB * 16, total = units * toks;
   const int l = threadIdx.x & 15;
-  for (int i0 = threadIdx.x & ~15; i0 < total; i0 += B * kW4Threads) {
+  for (int i0 = threadIdx.x; i0 - (int)(threadIdx.x & 31) < total; i0 += B * kW4Threads) {
     float v[B][8];
+    int tok[B], unit_of[B];
 #pragma unroll
-    for (int b = 0; b < B; ++b) {  // the loads of a few blocks in flight together
-      const int i = i0 + b * kW4Threads + l, m = i / units, u = i - m * units;
-      const int64_t k = ((int64_t)kb0 * 16 + u) * 8;
+    for (int b = 0; b < B; ++b) {  // the loads of B blocks in flight together
+      const int i = i0 + b * kW4Threads;
+      tok[b] = toks == 1 ? 0 : i / units;
+      unit_of[b] = i - tok[b] * units;
+      const int64_t k = ((int64_t)kb0 * 16 + unit_of[b]) * 8;
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[b][j] = 0.f;
       if (i < total && k < K) {
-        const T* p = X + (int64_t)m * K + k;
+        const T* p = X + (int64_t)tok[b] * K + k;
         if constexpr (sizeof(T) == 2) {
           const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
           const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -204,44 +241,55 @@ __device__ __forceinline__ void w4_stage_x(uint8_t* smem, const W4Smem& L, const
     }
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      const int i = i0 + b * kW4Threads;  // the block's first unit
-      if (i >= total) break;              // the same for its sixteen lanes
-      const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
-      const int m = i / units, u = i - m * units, kb = u >> 4;
+      const int i = i0 + b * kW4Threads;
+      if (i - (int)(threadIdx.x & 31) >= total) break;  // the same for the warp
+      const int m = tok[b], kb = unit_of[b] >> 4;
       uint32_t top = 0;  // largest magnitude, as bits: an infinity or NaN stays on top
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[b][j]) & 0x7FFFFFFFu);
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+      for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       // f = 2^e, at most 2^125: a block below 1e-31 keeps fewer bits
       const float f0 = __fdiv_rn(8323072.0f, fmaxf(__uint_as_float(top), 1e-31f));
-      const float f = __uint_as_float(__float_as_uint(f0) & 0xFF800000u);
-      // an infinity or NaN makes the token's results NaN
-      const float unit = top < 0x7F800000u ? __fdiv_rn(1.0f, f) : __uint_as_float(0x7FFFFFFFu);
+      const uint32_t fb = __float_as_uint(f0) & 0xFF800000u;
+      const float f = __uint_as_float(fb);
+      // 1/f, its exponent mirrored; an infinity or NaN makes the token's results NaN
+      const float unit = __uint_as_float(top < 0x7F800000u ? 0x7F000000u - fb : 0x7FFFFFFFu);
+      int fixed = 0;
       uint32_t w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        w[j] = ((uint32_t)__float2int_rn(__fmul_rn(v[b][j], f)) + 0x808080u) ^ 0x808080u;
-      uint32_t lane_off = kb * 128 + (l & 3) * 32 + (l >> 2) * 8;  // [t][u][8 bytes]
+      for (int j = 0; j < 8; ++j) {
+        const int n = __float2int_rn(__fmul_rn(v[b][j], f));
+        fixed += n;
+        w[j] = ((uint32_t)n + 0x808080u) ^ 0x808080u;
+      }
 #pragma unroll
-      for (int d = 0; d < 3; ++d) {  // digit d: byte d of the eight words
-        const uint32_t sel = d | ((4 + d) << 4);
-        const uint32_t a04 = __byte_perm(w[0], w[4], sel), a15 = __byte_perm(w[1], w[5], sel);
-        const uint32_t a26 = __byte_perm(w[2], w[6], sel), a37 = __byte_perm(w[3], w[7], sel);
-        const uint32_t b0 = __byte_perm(a04, a15, 0x5410), b1 = __byte_perm(a26, a37, 0x5410);
-        // columns of the MMA: digit d of token m
-        const int pc = 2 - d;  // the highest digit first
-        const int xc = m * 3 + pc;
-        const int col = PL ? (m >> 3) * 24 + pc * 8 + (m & 7) : xc;
-        *reinterpret_cast<uint2*>(smem + L.x + xc * L.x_stride + lane_off) = make_uint2(b0, b1);
-        int s = dp4a(b1, 0x01010101u, dp4a(b0, 0x01010101u, 0));
+      for (int o = 1; o < GL; o <<= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
+      if (i < total) {
+        const uint32_t lane_off = kb * 128 + (l & 3) * 32 + (l >> 2) * 8;  // [t][u][8 bytes]
 #pragma unroll
-        for (int o = 1; o < GL; o <<= 1) s += __shfl_xor_sync(mask, s, o);
-        if (l % GL == 0)
-          reinterpret_cast<int*>(smem + L.dsum)[(kb * V + l / GL) * COLS + col] = s;
-        if (l == d)
-          reinterpret_cast<float*>(smem + L.cf)[kb * COLS + col] =
-              __fmul_rn(unit, d == 2 ? 65536.0f : (d == 1 ? 256.0f : 1.0f));
+        for (int d = 0; d < 3; ++d) {  // digit d: byte d of the eight words
+          const uint32_t sel = d | ((4 + d) << 4);
+          const uint32_t a04 = __byte_perm(w[0], w[4], sel), a15 = __byte_perm(w[1], w[5], sel);
+          const uint32_t a26 = __byte_perm(w[2], w[6], sel), a37 = __byte_perm(w[3], w[7], sel);
+          *reinterpret_cast<uint2*>(smem + L.x + (m * 3 + 2 - d) * L.x_stride + lane_off) =
+              make_uint2(__byte_perm(a04, a15, 0x5410), __byte_perm(a26, a37, 0x5410));
+        }
+        // The group's sum (|sum| ≤ 128·2^23) goes with the token, or with its
+        // lowest digit's column, which counts 1.
+        if (l % GL == 0) {
+          float* s = dsum + (kb * V + l / GL) * SUMS + (PL ? m : 3 * m);
+          if (!PL) s[0] = s[1] = 0.f;
+          s[PL ? 0 : 2] = (float)fixed;
+        }
+        if (l == 0) {
+          float* c = cf + kb * SUMS + (PL ? m : 3 * m);
+          if (!PL) {
+            c[0] = __fmul_rn(unit, 65536.0f);
+            c[1] = __fmul_rn(unit, 256.0f);
+          }
+          c[PL ? 0 : 2] = unit;
+        }
       }
     }
   }
@@ -265,24 +313,25 @@ __device__ __forceinline__ void w4_stage_x(uint8_t* smem, const W4Smem& L, const
 template <typename T, int V, int NT>
 __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Params p) {
   using C = W4Pass<NT>;
-  constexpr int SUMS = C::kSums, COLS = C::kCols, TOK = C::kTok, ST = w4_stage_bytes<V>();
+  constexpr int SUMS = C::kSums, TOK = C::kTok, ST = w4_stage_bytes<V>();
   constexpr int NA = SUMS / 8;                  // accumulator tiles
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int D = p.stages, ranks = (int)cluster_size(), rank = (int)cluster_rank();
+  constexpr int D = w4_stages<V>();
+  const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
   // Blocks are counted in 32 bits: 2^31 of them are 2 TB.
-  const int RB = (int)((p.N + 15) / 16), KBt = (int)((p.K + 127) / 128);
-  const int slab = (int)blockIdx.x / ranks;
-  const int rb0 = (int)((int64_t)RB * slab / p.slabs), rb1 = (int)((int64_t)RB * (slab + 1) / p.slabs);
+  const int KBt = (int)((p.K + 127) / 128);
+  const int slab = (int)blockIdx.x >> (31 - __clz(ranks));  // ranks is a power of two
+  const int rb0 = slab * p.slab_rows + min(slab, p.slab_more);
+  const int nrb = p.slab_rows + (slab < p.slab_more ? 1 : 0);
   const int kb0 = KBt * rank / ranks, KB = KBt * (rank + 1) / ranks - kb0;
-  const int nrb = rb1 - rb0, items = nrb * KB;
-  const int it0 = (int)((int64_t)items * warp / kW4Warps);
-  const int it1 = (int)((int64_t)items * (warp + 1) / kW4Warps);
+  const int items = nrb * KB;
+  const int it0 = items * warp / kW4Warps, it1 = items * (warp + 1) / kW4Warps;
   const int64_t m0 = (int64_t)blockIdx.y * TOK;
   const int toks = (int)min((int64_t)TOK, p.M - m0);
-  const W4Smem L = w4_smem<V, NT>((KBt + ranks - 1) / ranks, (RB + p.slabs - 1) / p.slabs,
-                                  (int)min((int64_t)TOK, p.M), D);
+  const W4Smem L = w4_smem<V, NT>((KBt + ranks - 1) / ranks, p.slab_rows + (p.slab_more > 0 ? 1 : 0),
+                                  (int)min((int64_t)TOK, p.M), ranks);
   float* part = reinterpret_cast<float*>(smem + L.part);
   float* out = reinterpret_cast<float*>(smem + L.out);
 
@@ -291,39 +340,34 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
   // per lane, and 32·V bytes of scales and 16·V of zero points by the first
   // lanes. The first ones go out before the wait for the previous kernel,
   // which does not write the weights.
-  const bool is_scale = lane < 2 * V, has_aux = is_scale || (lane < 3 * V && p.zeros != nullptr);
+  const bool is_scale = lane < 2 * V;
+  const int has_aux = is_scale || (lane < 3 * V && p.zeros != nullptr);
   const uint32_t aux_step = is_scale ? 32 * V : 16 * V;
-  int q_kb = KB > 0 ? it0 % KB : 0;
-  const int64_t first = (int64_t)(rb0 + (KB > 0 ? it0 / KB : 0)) * KBt + kb0 + q_kb;
-  const uint8_t* w_src = p.W4 + first * 1024 + 16 * lane;
-  const uint8_t* aux_src = (is_scale ? reinterpret_cast<const uint8_t*>(p.scales) + 16 * lane
-                                     : p.zeros + 16 * (lane - 2 * V)) +
-                           first * aux_step;
-  const uint32_t ring = smem_u32(smem) + L.ring + warp * (D * ST), ring_end = ring + D * ST;
-  uint32_t q_dst = ring;
-  int left = it1 - it0;
-  auto request = [&]() {
-    if (left > 0) {
-      cp_async16(q_dst + 16 * lane, w_src);
-      cp_async16(q_dst + 16 * lane + 512, w_src + 512);
-      if (has_aux) cp_async16(q_dst + 16 * lane + 1024, aux_src);
-      int step = 1;
-      if (++q_kb == KB) {  // on to the next row block, past the other CTAs' blocks
-        q_kb = 0;
-        step += KBt - KB;
-      }
-      w_src += step * 1024;
-      aux_src += step * aux_step;
-      q_dst += ST;
-      if (q_dst == ring_end) q_dst = ring;
-      --left;
+  const uint8_t* w_src = p.W4 + 16 * lane;
+  const uint8_t* aux_src = is_scale ? reinterpret_cast<const uint8_t*>(p.scales) + 16 * lane
+                                    : p.zeros + 16 * (lane - 2 * V);
+  const uint32_t ring = smem_u32(smem) + L.ring + warp * (D * ST);
+  int q_kb = it0 % KB, left = it1 - it0;  // every CTA has a block of K: clusters are for long rows
+  uint32_t q_blk = (uint32_t)(rb0 + it0 / KB) * KBt + kb0 + q_kb;
+  auto request = [&](uint32_t dst) {
+    w4_request(dst + 16 * lane, w_src + (uint64_t)q_blk * 1024u, aux_src + (uint64_t)q_blk * aux_step,
+               left, has_aux);
+    --left;
+    ++q_blk;
+    if (++q_kb == KB) {  // on to the next row block, past the other CTAs' blocks
+      q_kb = 0;
+      q_blk += KBt - KB;
     }
-    cp_async_commit();
   };
-  for (int d = 0; d < D - 1; ++d) request();
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) request(ring + d * ST);
   pdl_wait_prior_grid();
 
-  w4_stage_x<T, V, NT>(smem, L, reinterpret_cast<const T*>(p.X) + m0 * p.K, p.K, kb0, KB, toks);
+  const T* X = reinterpret_cast<const T*>(p.X) + m0 * p.K;
+  if (KB * 16 * toks <= kW4Threads)
+    w4_stage_x<T, V, NT, 1>(smem, L, X, p.K, kb0, KB, toks);
+  else
+    w4_stage_x<T, V, NT, 4>(smem, L, X, p.K, kb0, KB, toks);
   if (it0 == it1)  // fewer blocks than warps: an empty run adds nothing
     for (int j = lane; j < 16 * SUMS; j += 32) part[warp * 32 * SUMS + j] = 0.f;
   __syncthreads();
@@ -341,25 +385,23 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
     xaddr[n] = smem_u32(smem) + L.x + xc * L.x_stride + 32 * t;
   }
   const uint32_t dsum = smem_u32(smem) + L.dsum + 8 * t, cf = smem_u32(smem) + L.cf + 8 * t;
+  const bool zs = p.zeros != nullptr;
+  const int magic[4] = {0x4B400000, 0x4B400000, 0x4B400000, 0x4B400000};
 
-  uint32_t src = ring;
-  int rb = KB > 0 ? it0 / KB : 0, kb = it0 - rb * KB, slot = 0;
+  uint32_t src = ring, last = ring + (D - 1) * ST;  // the next stage, the one before it
+  int rb = it0 / KB, kb = it0 - rb * KB, slot = 0;
   for (int it = it0; it < it1;) {
     const int begin = kb, end = min(KB, kb + (it1 - it));  // this run's part of row block rb
     float acc[NA][4];
 #pragma unroll
     for (int n = 0; n < NA; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+    uint32_t x_off = kb * 128, ds_at = dsum + kb * (V * SUMS * 4), cf_at = cf + kb * (SUMS * 4);
     for (; kb < end; ++kb) {
       // D − 1 blocks are under way; the oldest is next. Past the barrier every
       // lane sees it and is done with the stage before it, which is filled anew.
-      if (D == 4)
-        cp_async_wait<2>();
-      else if (D == 3)
-        cp_async_wait<1>();
-      else
-        cp_async_wait<0>();
+      cp_async_wait<D - 2>();
       __syncwarp();
-      request();
+      request(last);
       const uint4 wlo = lds128(src + 16 * lane), whi = lds128(src + 16 * lane + 512);
       const uint32_t lo[4] = {wlo.x, wlo.y, wlo.z, wlo.w}, hi[4] = {whi.x, whi.y, whi.z, whi.w};
       uint32_t a[4][4];
@@ -370,57 +412,65 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
         a[u][2] = (lo[u] >> 4) & 0x0F0F0F0Fu;
         a[u][3] = (hi[u] >> 4) & 0x0F0F0F0Fu;
       }
-      float s0[V], s1[V];
-      int z0[V], z1[V];
+      float s0[V], s1[V], z0[V], z1[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const uint32_t s = lds_u32(src + 1024 + (g * V + v) * 4);
         s0[v] = __uint_as_float(s << 16);
         s1[v] = __uint_as_float(s & 0xFFFF0000u);
-        const uint32_t z = p.zeros != nullptr ? lds_u16(src + 1024 + 32 * V + (g * V + v) * 2) : 0x0808u;
-        z0[v] = -(int)(z & 0xFFu);
-        z1[v] = -(int)(z >> 8);
+        uint32_t z = 0x0808u;
+        if (zs) z = lds_u16(src + 1024 + 32 * V + (g * V + v) * 2);
+        // 2^23 + z has z in its low bits
+        z0[v] = 8388608.0f - __uint_as_float(0x4B000000u | (z & 0xFFu));
+        z1[v] = 8388608.0f - __uint_as_float(0x4B000000u | (z >> 8));
       }
 #pragma unroll
       for (int n = 0; n < NA; ++n) {
         constexpr int ND = C::kPlanar ? 3 : 1;  // tiles of this accumulator: digits, or one
+        // The sums start at the bits of the float 1.5·2^23: what they end as, read
+        // as a float, less 1.5·2^23 is the sum (|sum| < 2^18).
         int d[ND][V][4];
-        float f[ND][2];
 #pragma unroll
         for (int j = 0; j < ND; ++j) {
           const int tile = n * ND + j;
-          const uint4 x0 = lds128(xaddr[tile] + kb * 128), x1 = lds128(xaddr[tile] + kb * 128 + 16);
+          const uint4 x0 = lds128(xaddr[tile] + x_off), x1 = lds128(xaddr[tile] + x_off + 16);
           const uint32_t b[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            // −z·Σd on top of the bits of 1.5·2^23: after the MMAs the float with
-            // these bits, less 1.5·2^23, is the sum (|sum| < 2^19)
-            const uint32_t o = dsum + ((kb * V + v) * COLS + 8 * tile) * 4;
-            const int ds0 = (int)lds_u32(o), ds1 = (int)lds_u32(o + 4);
-            d[j][v][0] = ds0 * z0[v] + 0x4B400000;
-            d[j][v][1] = ds1 * z0[v] + 0x4B400000;
-            d[j][v][2] = ds0 * z1[v] + 0x4B400000;
-            d[j][v][3] = ds1 * z1[v] + 0x4B400000;
 #pragma unroll
-            for (int u = v * (4 / V); u < (v + 1) * (4 / V); ++u)
-              mma_u8s8_16832(d[j][v], a[u][0], a[u][1], a[u][2], a[u][3], b[2 * u], b[2 * u + 1]);
+            for (int u = v * (4 / V); u < (v + 1) * (4 / V); ++u) {
+              if (u == v * (4 / V))
+                mma_u8s8_16832(d[j][v], a[u][0], a[u][1], a[u][2], a[u][3], b[2 * u], b[2 * u + 1], magic);
+              else
+                mma_u8s8_16832(d[j][v], a[u][0], a[u][1], a[u][2], a[u][3], b[2 * u], b[2 * u + 1], d[j][v]);
+            }
           }
-          f[j][0] = __uint_as_float(lds_u32(cf + (kb * COLS + 8 * tile) * 4));
-          f[j][1] = __uint_as_float(lds_u32(cf + (kb * COLS + 8 * tile) * 4 + 4));
         }
+        const uint2 cq = lds64(cf_at + 32 * n);
+        const float c0 = __uint_as_float(cq.x), c1 = __uint_as_float(cq.y);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+          const uint2 dq = lds64(ds_at + (v * SUMS + 8 * n) * 4);
+          const float t0 = __uint_as_float(dq.x), t1 = __uint_as_float(dq.y);
+          float y[4];
 #pragma unroll
-          for (int j = ND - 1; j >= 0; --j) {
-            acc[n][0] = fmaf(__int_as_float(d[j][v][0]) - 12582912.0f, s0[v] * f[j][0], acc[n][0]);
-            acc[n][1] = fmaf(__int_as_float(d[j][v][1]) - 12582912.0f, s0[v] * f[j][1], acc[n][1]);
-            acc[n][2] = fmaf(__int_as_float(d[j][v][2]) - 12582912.0f, s1[v] * f[j][0], acc[n][2]);
-            acc[n][3] = fmaf(__int_as_float(d[j][v][3]) - 12582912.0f, s1[v] * f[j][1], acc[n][3]);
+          for (int e = 0; e < 4; ++e) {
+            y[e] = __int_as_float(d[0][v][e]) - 12582912.0f;
+#pragma unroll
+            for (int j = 1; j < ND; ++j) y[e] = fmaf(y[e], 256.0f, __int_as_float(d[j][v][e]) - 12582912.0f);
           }
+          // less z times the activations' sum, then the scales
+          acc[n][0] = fmaf(fmaf(z0[v], t0, y[0]), s0[v] * c0, acc[n][0]);
+          acc[n][1] = fmaf(fmaf(z0[v], t1, y[1]), s0[v] * c1, acc[n][1]);
+          acc[n][2] = fmaf(fmaf(z1[v], t0, y[2]), s1[v] * c0, acc[n][2]);
+          acc[n][3] = fmaf(fmaf(z1[v], t1, y[3]), s1[v] * c1, acc[n][3]);
         }
       }
-      src += ST;
-      if (src == ring_end) src = ring;
+      x_off += 128;
+      ds_at += V * SUMS * 4;
+      cf_at += SUMS * 4;
+      last = src;
+      src = src == ring + (D - 1) * ST ? ring : src + ST;
     }
     it += end - begin;
     // The share of row block rb: slot 0 for the run's first, 1 for a later one.
@@ -432,8 +482,13 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
     }
     if (begin == 0 && end == KB) {  // whole
       __syncwarp();
-      for (int j = lane; j < 16 * toks; j += 32)
-        out[rb * toks * 16 + j] = w4_gather<NT>(part, warp, warp, warp * 2 + slot, j & 15, j >> 4);
+      for (int j = lane; j < 16 * toks; j += 32) {
+        const float y = w4_gather<NT>(part, warp, warp, warp * 2 + slot, j & 15, j >> 4);
+        if (ranks > 1)
+          out[rb * toks * 16 + j] = y;
+        else
+          w4_store(p, rb0 + rb, m0, j, y);
+      }
       __syncwarp();
     } else {
       slot = 1;
@@ -443,43 +498,33 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
   }
   __syncthreads();
   // Row blocks that several runs share.
-  for (int j = tid; j < nrb * 16 * toks; j += kW4Threads) {
-    const int r = j / (16 * toks);
-    if (KB == 0) {
-      out[j] = 0.f;
-      continue;
-    }
+  for (int r = warp; r < nrb; r += kW4Warps) {
     const int w_lo = w4_warp_of(r * KB, items), w_hi = w4_warp_of(r * KB + KB - 1, items);
     if (w_lo == w_hi) continue;
     // the first of them may have begun in an earlier row block
-    const int started = (int)((int64_t)items * w_lo / kW4Warps);
-    const int i = j - r * 16 * toks;
-    out[j] = w4_gather<NT>(part, w_lo, w_hi, w_lo * 2 + (started < r * KB ? 1 : 0), i & 15, i >> 4);
-  }
-  __syncwarp();
-  if (ranks > 1)
-    cluster_barrier();
-  else
-    __syncthreads();
-  const int rows = nrb * 16;
-  for (int j = tid + rank * kW4Threads; j < rows * toks; j += kW4Threads * ranks) {
-    const int c = j / rows, r = j - c * rows, o = ((r >> 4) * toks + c) * 16 + (r & 15);
-    float y = 0.f;
-    if (ranks > 1) {
-      for (int k = 0; k < ranks; ++k) y += cluster_lds_f32(smem_u32(out + o), k);
-    } else {
-      y = out[o];
-    }
-    const int64_t row = (int64_t)rb0 * 16 + r, at = (m0 + c) * p.N + row;
-    if (row < p.N) {
-      if (p.y_bf16)
-        reinterpret_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(y);
+    const int slot_lo = w_lo * 2 + (items * w_lo / kW4Warps < r * KB ? 1 : 0);
+    for (int j = lane; j < 16 * toks; j += 32) {
+      const float y = w4_gather<NT>(part, w_lo, w_hi, slot_lo, j & 15, j >> 4);
+      if (ranks > 1)
+        out[r * toks * 16 + j] = y;
       else
-        reinterpret_cast<float*>(p.Y)[at] = y;
+        w4_store(p, rb0 + r, m0, j, y);
     }
   }
-  __syncwarp();
-  if (ranks > 1) cluster_barrier();  // the others may still read this CTA's sums
+  if (ranks > 1) {
+    __syncwarp();
+    cluster_barrier();
+    for (int r = warp * ranks + rank; r < nrb; r += kW4Warps * ranks) {
+      for (int j = lane; j < 16 * toks; j += 32) {
+        const uint32_t o = smem_u32(out + r * toks * 16 + j);
+        float y = 0.f;
+        for (int k = 0; k < ranks; ++k) y += cluster_lds_f32(o, k);
+        w4_store(p, rb0 + r, m0, j, y);
+      }
+    }
+    __syncwarp();
+    cluster_barrier();  // the others may still read this CTA's sums
+  }
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
