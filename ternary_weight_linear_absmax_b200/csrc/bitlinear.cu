@@ -949,29 +949,82 @@ bl_status launch_w4(const W4Params& p, int group, bool pdl, int dev, int sms, cu
 
 // --------------------------------------------------------------------------
 // Layer norm and 8-bit checkpoints.
-template <typename T>
-bl_status launch_norm(const NormParams& p, int out, cudaStream_t st) {
-  const dim3 grid((unsigned)p.M);
-  if (out == 0)
-    layernorm_kernel<T, float><<<grid, kNormThreads, 0, st>>>(p);
-  else if (out == 1)
-    layernorm_kernel<T, __nv_bfloat16><<<grid, kNormThreads, 0, st>>>(p);
-  else
-    layernorm_kernel<T, int8_t><<<grid, kNormThreads, 0, st>>>(p);
+// Units of eight columns per thread and threads per row: few units while the
+// row fits 512 threads.
+struct NormShape {
+  int nu, group;  // nu 0: the row is too long for registers
+};
+NormShape norm_shape(int64_t K) {
+  const int64_t units = K / 8;
+  const int nu = units <= 128 ? 1 : units <= 1024 ? 2 : units <= 2048 ? 4 : 0;
+  if (nu == 0) return {0, 0};
+  return {nu, (int)((((units + nu - 1) / nu) + 31) / 32 * 32)};
+}
+
+template <typename T, typename OUT>
+bl_status launch_norm_out(const NormParams& p, cudaStream_t st) {
+  const NormShape s = norm_shape(p.K);
+  if (s.nu == 0) {
+    layernorm_long_kernel<T, OUT><<<(unsigned)p.M, kNormThreads, 0, st>>>(p);
+  } else {
+    const int groups = s.group >= 128 ? 1 : 128 / s.group;  // at least 128 threads to a CTA
+    const dim3 grid((unsigned)((p.M + groups - 1) / groups)), block(groups * s.group);
+    if (s.nu == 1)
+      layernorm_kernel<T, OUT, 1><<<grid, block, 0, st>>>(p, s.group);
+    else if (s.nu == 2)
+      layernorm_kernel<T, OUT, 2><<<grid, block, 0, st>>>(p, s.group);
+    else
+      layernorm_kernel<T, OUT, 4><<<grid, block, 0, st>>>(p, s.group);
+  }
   BL_CUDA(cudaGetLastError());
   return BL_OK;
+}
+template <typename T>
+bl_status launch_norm(const NormParams& p, int out, cudaStream_t st) {
+  if (out == 0) return launch_norm_out<T, float>(p, st);
+  if (out == 1) return launch_norm_out<T, __nv_bfloat16>(p, st);
+  return launch_norm_out<T, int8_t>(p, st);
 }
 
 inline int64_t norm_grad_parts(int64_t M) { return M < kNormGradParts ? M : kNormGradParts; }
 
-template <typename TD, typename TX>
-bl_status launch_norm_grad(const NormGradParams& p, bl_dtype dx_dtype, int grid, cudaStream_t st) {
-  if (dx_dtype == BL_BF16)
-    layernorm_grad_kernel<TD, TX, __nv_bfloat16><<<grid, kNormThreads, 0, st>>>(p);
-  else
-    layernorm_grad_kernel<TD, TX, float><<<grid, kNormThreads, 0, st>>>(p);
+template <typename TD, typename TX, typename TO, int NU>
+bl_status launch_norm_grad_nu(const NormGradParams& p, int grid, int dev, cudaStream_t st) {
+  const int64_t units = p.K / 8;
+  const int group = (int)(((units + NU - 1) / NU + 31) / 32 * 32);
+  int groups = (NU == 1 ? 1024 : 512) / group;
+  if (groups > 15 && group > 32) groups = 15;  // a named barrier each
+  const int64_t rows = (p.M + grid - 1) / grid;
+  if (groups > rows) groups = (int)rows;
+  const int stage = norm_stage_bytes<TD, TX, NU>(group) * groups;
+  const int stages = stage * 4 <= 200 * 1024 ? 4 : stage * 3 <= 200 * 1024 ? 3 : 2;
+  size_t smem = (size_t)stage * stages;
+  const size_t share = (size_t)groups * 2 * p.K * 4;
+  if (smem < share) smem = share;
+  auto* k = layernorm_grad_kernel<TD, TX, TO, NU>;
+  BL_TRY(ensure_smem(k, dev, smem));
+  k<<<grid, groups * group, smem, st>>>(p, group, stages);
   BL_CUDA(cudaGetLastError());
   return BL_OK;
+}
+
+template <typename TD, typename TX, typename TO>
+bl_status launch_norm_grad_out(const NormGradParams& p, int grid, int dev, cudaStream_t st) {
+  if (p.K <= 4096) return launch_norm_grad_nu<TD, TX, TO, 1>(p, grid, dev, st);
+  if (p.K <= 8192) return launch_norm_grad_nu<TD, TX, TO, 2>(p, grid, dev, st);
+  // two ring stages of the row have to fit in shared memory
+  if (p.K <= 16384 && 2 * norm_stage_bytes<TD, TX, 4>((int)((p.K / 32 + 31) / 32 * 32)) <= 226 * 1024)
+    return launch_norm_grad_nu<TD, TX, TO, 4>(p, grid, dev, st);
+  layernorm_grad_long_kernel<TD, TX, TO><<<grid, kNormThreads, 0, st>>>(p);
+  BL_CUDA(cudaGetLastError());
+  return BL_OK;
+}
+
+template <typename TD, typename TX>
+bl_status launch_norm_grad(const NormGradParams& p, bl_dtype dx_dtype, int grid, int dev,
+                           cudaStream_t st) {
+  return dx_dtype == BL_BF16 ? launch_norm_grad_out<TD, TX, __nv_bfloat16>(p, grid, dev, st)
+                             : launch_norm_grad_out<TD, TX, float>(p, grid, dev, st);
 }
 
 // The two forms of the backward: from the input (x_dtype fp32/bf16) or from
@@ -1025,14 +1078,14 @@ bl_status norm_grad_impl(const void* dY, bl_dtype dy_dtype, const void* X, int x
   const bool db = dy_dtype == BL_BF16;
   if (x_dtype < 0)
     BL_TRY((db ? launch_norm_grad<__nv_bfloat16, int8_t> : launch_norm_grad<float, int8_t>)(
-        p, dx_dtype, grid, st));
+        p, dx_dtype, grid, dev, st));
   else if (x_dtype == BL_BF16)
     BL_TRY((db ? launch_norm_grad<__nv_bfloat16, __nv_bfloat16>
-               : launch_norm_grad<float, __nv_bfloat16>)(p, dx_dtype, grid, st));
+               : launch_norm_grad<float, __nv_bfloat16>)(p, dx_dtype, grid, dev, st));
   else
     BL_TRY((db ? launch_norm_grad<__nv_bfloat16, float> : launch_norm_grad<float, float>)(
-        p, dx_dtype, grid, st));
-  norm_colsum_kernel<<<(unsigned)((2 * K + 255) / 256), 256, 0, st>>>(p.part, grid, K, dweight, dbias);
+        p, dx_dtype, grid, dev, st));
+  norm_colsum_kernel<<<(unsigned)(2 * K / 32), 256, 0, st>>>(p.part, grid, K, dweight, dbias);
   BL_CUDA(cudaGetLastError());
   return BL_OK;
 }

@@ -20,6 +20,7 @@
 namespace bl {
 
 constexpr int kNormThreads = 256;
+constexpr int kNormMaxThreads = 512;
 constexpr float kCkptTiny = 7.888609052210118e-31f;  // 2^-100
 
 // Eight consecutive elements as fp32.
@@ -152,9 +153,170 @@ __device__ __forceinline__ void norm_affine8(const float (&x)[8], float mean, fl
   }
 }
 
-// OUT: fp32/bf16 rows, or int8_t for the tokens.
+// Threads that share a row. A CTA holds blockDim.x / T such groups; with T = 32
+// a group is a warp and needs no barrier; there are at most 15 larger ones.
+struct RowGroup {
+  int T, id, tid, warps;  // threads, which group, thread in it, its warps
+  __device__ __forceinline__ explicit RowGroup(int t)
+      : T(t), id((int)threadIdx.x / t), tid((int)threadIdx.x % t), warps(t >> 5) {}
+  __device__ __forceinline__ void sync() const {
+    if (T == 32)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(T) : "memory");  // 0 is the CTA's
+  }
+};
+
+// Values of the group's warps, combined in a fixed order and returned to all.
+// `buf` is one of several buffers of 32 values per CTA, not used again before
+// another of the group's barriers.
+template <typename T, typename Op>
+__device__ __forceinline__ T group_reduce(const RowGroup& g, T v, T* buf, Op op) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (g.T == 32) return v;
+  T* mine = buf + (g.id * g.T >> 5);
+  if ((threadIdx.x & 31) == 0) mine[g.tid >> 5] = v;
+  g.sync();
+  v = mine[0];
+  for (int w = 1; w < g.warps; ++w) v = op(v, mine[w]);
+  return v;
+}
+
+// Eight raw elements of a row, as loaded.
+template <typename T>
+struct Raw8 {
+  uint4 a[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) a[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      const uint32_t w[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 2) {
+          v[2 * j] = __uint_as_float(w[j] << 16);
+          v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        } else {
+          v[4 * i + j] = __uint_as_float(w[j]);
+        }
+      }
+    }
+  }
+};
+
+// One row per group of T threads, NU units of eight columns per thread, the
+// row in registers between the passes. OUT: fp32/bf16 rows, or int8_t for the
+// tokens.
+template <typename T, typename OUT, int NU>
+__global__ void __launch_bounds__(kNormMaxThreads) layernorm_kernel(const NormParams p, int group) {
+  __shared__ double redd[2][32];
+  __shared__ float redf[32];
+  __shared__ int redi[32];
+  const RowGroup g(group);
+  const int64_t m = (int64_t)blockIdx.x * (blockDim.x / group) + g.id;
+  if (m >= p.M) return;  // whole groups
+  const int units = (int)(p.K / 8);
+  const T* row = reinterpret_cast<const T*>(p.X) + m * p.K;
+  Raw8<T> raw[NU];
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int u = g.tid + i * g.T;
+    if (u < units) raw[i].load(row + 8 * u);
+  }
+  float x[8];
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    if (g.tid + i * g.T < units) {
+      raw[i].get(x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += (double)x[j];
+    }
+  }
+  auto add = [](auto a, auto b) { return a + b; };
+  const float mean = (float)(group_reduce(g, s, redd[0], add) / (double)p.K);
+  s = 0.0;
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    if (g.tid + i * g.T < units) {
+      raw[i].get(x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double d = (double)__fsub_rn(x[j], mean);
+        s = fma(d, d, s);
+      }
+    }
+  }
+  const float rstd =
+      (float)(1.0 / sqrt(group_reduce(g, s, redd[1], add) / (double)p.K + (double)p.eps));
+  if (g.tid == 0) {
+    if (p.mean != nullptr) p.mean[m] = mean;
+    if (p.rstd != nullptr) p.rstd[m] = rstd;
+  }
+  float xhat[8], y[8];
+  if constexpr (sizeof(OUT) > 1) {
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int u = g.tid + i * g.T;
+      if (u < units) {
+        raw[i].get(x);
+        norm_affine8(x, mean, rstd, p.weight, p.bias, 8 * u, xhat, y);
+        norm_store8(reinterpret_cast<OUT*>(p.Y) + m * p.K + 8 * u, y);
+      }
+    }
+  } else {
+    float mx = 0.f, keep[NU][8];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {  // whole warps: a checkpoint group is eight lanes
+      const int u = g.tid + i * g.T;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) xhat[j] = 0.f;
+      if (u < units) {
+        raw[i].get(x);
+        norm_affine8(x, mean, rstd, p.weight, p.bias, 8 * u, xhat, keep[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(keep[i][j]));
+      }
+      if (p.xq != nullptr) {
+        uint32_t w0, w1;
+        const float sc = ckpt_codes8<true>(xhat, w0, w1);
+        if (u < units) {
+          *reinterpret_cast<uint2*>(p.xq + m * p.K + 8 * u) = make_uint2(w0, w1);
+          if ((u & 7) == 0) p.xs[(m * p.K + 8 * u) / 64] = sc;
+        }
+      }
+    }
+    mx = group_reduce(g, mx, redf, [](float a, float b) { return fmaxf(a, b); });
+    const float scale = __fdiv_rn(127.0f, __fadd_rn(mx, p.q_eps));
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int u = g.tid + i * g.T;
+      if (u < units) {
+        uint32_t b[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = quant_i8_bits(keep[i][j], scale);
+        const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
+        const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
+        sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
+        *reinterpret_cast<uint2*>(p.Aq + m * p.K + 8 * u) = make_uint2(w0, w1);
+      }
+    }
+    if (p.rowsum != nullptr) sum = group_reduce(g, sum, redi, add);
+    if (g.tid == 0) {
+      p.gamma[m] = mx;
+      if (p.rowsum != nullptr) p.rowsum[m] = sum;
+    }
+  }
+}
+
+// Rows longer than a CTA's registers hold: every pass reads the row again.
 template <typename T, typename OUT>
-__global__ void __launch_bounds__(kNormThreads) layernorm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const NormParams p) {
   __shared__ double redd[kNormThreads / 32];
   __shared__ float redf[kNormThreads / 32];
   const int64_t m = blockIdx.x, units = p.K / 8;
@@ -243,7 +405,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_kernel(const NormParam
 // Backward. Each CTA takes every gridDim.x-th row and writes its share of dw
 // and db into its own row of `part` (2·K floats); norm_colsum_kernel adds the
 // rows in a fixed order, so the result does not depend on timing.
-constexpr int kNormGradParts = 296;
+constexpr int kNormGradParts = 148;
 
 struct NormGradParams {
   const void* dY;      // [M, K]
@@ -257,6 +419,203 @@ struct NormGradParams {
   float* part;         // [grid, 2, K]
 };
 
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes) {
+  if (bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Bytes of one row in a ring stage, for one group of T threads: dY and X (or
+// the checkpoint) in pieces of 16 (8) bytes, piece-major, so that neighbouring
+// threads touch neighbouring pieces.
+template <typename TD, typename TX, int NU>
+__host__ __device__ constexpr int norm_stage_bytes(int T) {
+  return NU * T * 8 * (int)(sizeof(TD) + sizeof(TX));
+}
+
+// One row per group of T threads at a time, NU units of eight columns per
+// thread. A thread copies its own columns of the coming rows into its part of
+// the ring (cp.async: nobody else reads them, so no barrier guards the ring),
+// and keeps their shares of dw and db in registers; the two row sums are the
+// only thing that the group exchanges. The CTA's groups add up their shares in
+// shared memory at the end.
+template <typename TD, typename TX, typename TO, int NU>
+__global__ void __launch_bounds__(NU == 1 ? 1024 : 512)
+layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 red[2][32];
+  const RowGroup g(group);
+  const int groups = (int)blockDim.x / group, T = group, units = (int)(p.K / 8);
+  constexpr int PD = sizeof(TD) / 2;                      // 16-byte pieces of a unit of dY
+  constexpr int PX = sizeof(TX) == 1 ? 1 : sizeof(TX) / 2, XB = sizeof(TX) == 1 ? 8 : 16;
+  const int stage_bytes = norm_stage_bytes<TD, TX, NU>(T);
+  const uint32_t ring = smem_u32(smem) + g.id * stages * stage_bytes;
+  const uint32_t mine_d = ring + 16 * g.tid, mine_x = ring + NU * T * 16 * PD + XB * g.tid;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t next = (int64_t)g.id * gridDim.x + blockIdx.x;  // the next row to request
+  const int64_t first = next;
+  int q = 0;
+  auto request = [&]() {
+    if (next < p.M) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        const int u = g.tid + i * T;
+        if (u < units) {
+          const uint8_t* d = reinterpret_cast<const uint8_t*>(p.dY) + (next * p.K + 8 * u) * (int64_t)sizeof(TD);
+          const uint8_t* x = reinterpret_cast<const uint8_t*>(p.X) + (next * p.K + 8 * u) * (int64_t)sizeof(TX);
+#pragma unroll
+          for (int c = 0; c < PD; ++c)
+            cp_async(mine_d + q * stage_bytes + (i * PD + c) * T * 16, d + 16 * c, 16);
+#pragma unroll
+          for (int c = 0; c < PX; ++c)
+            cp_async(mine_x + q * stage_bytes + (i * PX + c) * T * XB, x + 16 * c, XB);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    next += step;
+    q = q + 1 == stages ? 0 : q + 1;
+  };
+  for (int s = 0; s < stages - 1; ++s) request();
+
+  float dw[NU][8], db[NU][8], w[NU][8];
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int u = g.tid + i * T;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = w[i][j] = 0.f;
+    if (NU < 4 && u < units) norm_load8(p.weight + 8 * u, w[i]);
+  }
+  auto get = [&](int stage, int i, float mean, float rstd, float xs, float (&dy)[8], float (&xh)[8]) {
+    const uint8_t* d = smem + (mine_d - smem_u32(smem)) + stage * stage_bytes;
+    const uint8_t* x = smem + (mine_x - smem_u32(smem)) + stage * stage_bytes;
+    if constexpr (PD == 1) {
+      Raw8<__nv_bfloat16> r;
+      r.a[0] = *reinterpret_cast<const uint4*>(d + i * T * 16);
+      r.get(dy);
+    } else {
+      Raw8<float> r;
+      r.a[0] = *reinterpret_cast<const uint4*>(d + (i * 2) * T * 16);
+      r.a[1] = *reinterpret_cast<const uint4*>(d + (i * 2 + 1) * T * 16);
+      r.get(dy);
+    }
+    if constexpr (sizeof(TX) == 1) {
+      const uint2 v = *reinterpret_cast<const uint2*>(x + i * T * 8);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        xh[j] = __fmul_rn((float)(int8_t)(((j < 4 ? v.x : v.y) >> (8 * (j & 3))) & 255u), xs);
+    } else {
+      Raw8<TX> r;
+#pragma unroll
+      for (int c = 0; c < PX; ++c) r.a[c] = *reinterpret_cast<const uint4*>(x + (i * PX + c) * T * 16);
+      r.get(xh);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) xh[j] = __fmul_rn(__fsub_rn(xh[j], mean), rstd);
+    }
+  };
+
+  int stage = 0, buf = 0;
+  const float inv_k = 1.0f / (float)p.K;
+  for (int64_t m = first; m < p.M; m += step) {
+    const float rstd = __ldg(p.rstd + m);
+    float mean = 0.f, xs[NU];
+    if constexpr (sizeof(TX) > 1) mean = __ldg(p.mean + m);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      xs[i] = 0.f;
+      if (sizeof(TX) == 1 && g.tid + i * T < units) xs[i] = __ldg(p.xs + (m * units + g.tid + i * T) / 8);
+    }
+    // The stage read last is this thread's own, and read.
+    request();
+    if (stages == 4)
+      asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (stages == 3)
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    float dy[NU][8], xh[NU][8];
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int u = g.tid + i * T;
+      if (u < units) {
+        get(stage, i, mean, rstd, xs[i], dy[i], xh[i]);
+        if (NU == 4) norm_load8(p.weight + 8 * u, w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          dw[i][j] = fmaf(dy[i][j], xh[i][j], dw[i][j]);
+          db[i][j] += dy[i][j];
+          const float gj = dy[i][j] * w[i][j];
+          a += gj;
+          b = fmaf(gj, xh[i][j], b);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (T > 32) {
+      float2* mine = red[buf] + (g.id * T >> 5);
+      if ((threadIdx.x & 31) == 0) mine[g.tid >> 5] = make_float2(a, b);
+      g.sync();  // one barrier per row: the buffers alternate
+      a = b = 0.f;
+      for (int k = 0; k < g.warps; ++k) {
+        const float2 v = mine[k];
+        a += v.x;
+        b += v.y;
+      }
+      buf ^= 1;
+    }
+    a *= inv_k;
+    b *= inv_k;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int u = g.tid + i * T;
+      if (u < units) {
+        if (NU == 4) {  // read again rather than kept
+          get(stage, i, mean, rstd, xs[i], dy[i], xh[i]);
+          norm_load8(p.weight + 8 * u, w[i]);
+        }
+        float dx[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dx[j] = rstd * fmaf(-xh[i][j], b, fmaf(dy[i][j], w[i][j], -a));
+        norm_store8(reinterpret_cast<TO*>(p.dX) + m * p.K + 8 * u, dx);
+      }
+    }
+    stage = stage + 1 == stages ? 0 : stage + 1;
+  }
+  // The groups' shares, [group][2][K] in what was the ring.
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  float* share = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int u = g.tid + i * T;
+    if (u < units) {
+      norm_store8(share + (int64_t)g.id * 2 * p.K + 8 * u, dw[i]);
+      norm_store8(share + (int64_t)g.id * 2 * p.K + p.K + 8 * u, db[i]);
+    }
+  }
+  __syncthreads();
+  float* out = p.part + (int64_t)blockIdx.x * 2 * p.K;
+  for (int c = 4 * (int)threadIdx.x; c < 2 * p.K; c += 4 * (int)blockDim.x) {
+    float4 s = *reinterpret_cast<const float4*>(share + c);
+    for (int k = 1; k < groups; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(share + (int64_t)k * 2 * p.K + c);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    *reinterpret_cast<float4*>(out + c) = s;
+  }
+}
+
+// Rows longer than a CTA's registers hold: the shares of dw and db live in the
+// workspace, and every pass reads the row again.
 // x̂ of eight columns: from the input, or from the checkpoint (TX = int8_t).
 template <typename TX>
 __device__ __forceinline__ void norm_xhat8(const NormGradParams& p, int64_t m, int64_t c,
@@ -273,7 +632,7 @@ __device__ __forceinline__ void norm_xhat8(const NormGradParams& p, int64_t m, i
 }
 
 template <typename TD, typename TX, typename TO>
-__global__ void __launch_bounds__(kNormThreads) layernorm_grad_kernel(const NormGradParams p) {
+__global__ void __launch_bounds__(kNormThreads) layernorm_grad_long_kernel(const NormGradParams p) {
   __shared__ float red[kNormThreads / 32];
   const int64_t units = p.K / 8;
   float* pw = p.part + (int64_t)blockIdx.x * 2 * p.K;
@@ -321,13 +680,22 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_grad_kernel(const Norm
   }
 }
 
+// dw and db from the CTAs' shares: 32 columns per CTA, eight threads per column
+// take every eighth share each, in order.
 __global__ void __launch_bounds__(256)
 norm_colsum_kernel(const float* __restrict__ part, int parts, int64_t K, float* __restrict__ dw,
                    float* __restrict__ db) {
-  const int64_t c = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;  // 0 .. 2K
-  if (c >= 2 * K) return;
+  __shared__ float red[8][32];
+  const int64_t c = blockIdx.x * (int64_t)32 + (threadIdx.x & 31);  // 0 .. 2K: a multiple of 32
+  const int k = threadIdx.x >> 5;
   float s = 0.f;
-  for (int i = 0; i < parts; ++i) s += part[(int64_t)i * 2 * K + c];
+#pragma unroll 4
+  for (int i = k; i < parts; i += 8) s += __ldg(part + (int64_t)i * 2 * K + c);
+  red[k][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (k != 0) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s += red[i][threadIdx.x];
   if (c < K)
     dw[c] = s;
   else if (db != nullptr)
