@@ -1010,7 +1010,7 @@ bl_status launch_norm_grad_nu(const NormGradParams& p, int grid, int dev, cudaSt
 
 template <typename TD, typename TX, typename TO>
 bl_status launch_norm_grad_out(const NormGradParams& p, int grid, int dev, cudaStream_t st) {
-  if (p.K <= 4096) return launch_norm_grad_nu<TD, TX, TO, 1>(p, grid, dev, st);
+  if (p.K <= 1024) return launch_norm_grad_nu<TD, TX, TO, 1>(p, grid, dev, st);
   if (p.K <= 8192) return launch_norm_grad_nu<TD, TX, TO, 2>(p, grid, dev, st);
   // two ring stages of the row have to fit in shared memory
   if (p.K <= 16384 && 2 * norm_stage_bytes<TD, TX, 4>((int)((p.K / 32 + 31) / 32 * 32)) <= 226 * 1024)
@@ -1085,9 +1085,8 @@ bl_status norm_grad_impl(const void* dY, bl_dtype dy_dtype, const void* X, int x
   else
     BL_TRY((db ? launch_norm_grad<__nv_bfloat16, float> : launch_norm_grad<float, float>)(
         p, dx_dtype, grid, dev, st));
-  norm_colsum_kernel<<<(unsigned)(2 * K / 32), 256, 0, st>>>(p.part, grid, K, dweight, dbias);
-  BL_CUDA(cudaGetLastError());
-  return BL_OK;
+  return launch_pdl(norm_colsum_kernel, dim3((unsigned)(2 * K / 32)), dim3(1024), st, p.part, grid, K,
+                    dweight, dbias);
 }
 
 inline int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
@@ -2090,6 +2089,7 @@ bl_status bl_layernorm(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, co
   p.bias = bias;
   p.M = M;
   p.K = K;
+  p.inv_k = 1.0 / (double)K;
   p.eps = eps;
   p.Y = Y;
   p.mean = mean;
@@ -2129,6 +2129,7 @@ bl_status bl_layernorm_quant(const void* X, bl_dtype x_dtype, int64_t M, int64_t
   p.bias = bias;
   p.M = M;
   p.K = K;
+  p.inv_k = 1.0 / (double)K;
   p.eps = eps;
   p.q_eps = q_eps;
   p.rstd = rstd;

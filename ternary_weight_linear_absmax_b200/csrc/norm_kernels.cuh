@@ -125,6 +125,7 @@ struct NormParams {
   const float* weight;  // [K]
   const float* bias;    // [K] or null
   int64_t M, K;
+  double inv_k;         // 1/K
   float eps, q_eps;
   void* Y;              // floats: [M, K]
   float* mean;          // [M] or null
@@ -183,6 +184,16 @@ __device__ __forceinline__ T group_reduce(const RowGroup& g, T v, T* buf, Op op)
   return v;
 }
 
+// 1/√v in 64 bits, rounded once to fp32: the fp32 estimate (2^-22) and two
+// Newton steps, each of which squares the error.
+__device__ __forceinline__ float rsqrt_once(double v) {
+  if (!(v > 1e-30 && v < 1e30)) return (float)(1.0 / sqrt(v));
+  double r = (double)rsqrtf((float)v);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = fma(0.5 * r, fma(-v * r, r, 1.0), r);
+  return (float)r;
+}
+
 // Eight raw elements of a row, as loaded.
 template <typename T>
 struct Raw8 {
@@ -238,7 +249,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) layernorm_kernel(const NormPa
     }
   }
   auto add = [](auto a, auto b) { return a + b; };
-  const float mean = (float)(group_reduce(g, s, redd[0], add) / (double)p.K);
+  const float mean = (float)(group_reduce(g, s, redd[0], add) * p.inv_k);
   s = 0.0;
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
@@ -251,8 +262,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) layernorm_kernel(const NormPa
       }
     }
   }
-  const float rstd =
-      (float)(1.0 / sqrt(group_reduce(g, s, redd[1], add) / (double)p.K + (double)p.eps));
+  const float rstd = rsqrt_once(fma(group_reduce(g, s, redd[1], add), p.inv_k, (double)p.eps));
   if (g.tid == 0) {
     if (p.mean != nullptr) p.mean[m] = mean;
     if (p.rstd != nullptr) p.rstd[m] = rstd;
@@ -328,7 +338,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
 #pragma unroll
     for (int j = 0; j < 8; ++j) s += (double)x[j];
   }
-  const float mean = (float)(block_sum_d(s, redd) / (double)p.K);
+  const float mean = (float)(block_sum_d(s, redd) * p.inv_k);
   s = 0.0;
   for (int64_t u = threadIdx.x; u < units; u += kNormThreads) {
     norm_load8(row + 8 * u, x);
@@ -338,7 +348,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
       s = fma(d, d, s);
     }
   }
-  const float rstd = (float)(1.0 / sqrt(block_sum_d(s, redd) / (double)p.K + (double)p.eps));
+  const float rstd = rsqrt_once(fma(block_sum_d(s, redd), p.inv_k, (double)p.eps));
   if (threadIdx.x == 0) {
     if (p.mean != nullptr) p.mean[m] = mean;
     if (p.rstd != nullptr) p.rstd[m] = rstd;
@@ -426,6 +436,26 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int byte
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// Sums of a and b over the warp, returned to all lanes. The first step leaves
+// a's halves to the lower lanes and b's to the upper ones, so that one value per
+// lane is left to add up.
+__device__ __forceinline__ void pair_sum(float& a, float& b) {
+  const bool up = (threadIdx.x & 16) != 0;
+  float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  a = __shfl_sync(0xffffffffu, v, 0);
+  b = __shfl_sync(0xffffffffu, v, 16);
+}
+
+// Four signed bytes as floats: byte ^ 0x80 in the low bits of 2^23.
+__device__ __forceinline__ void bytes_to_float(uint32_t w, float* v) {
+  w ^= 0x80808080u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 | j)) - 8388736.0f;
+}
+
 // Bytes of one row in a ring stage, for one group of T threads: dY and X (or
 // the checkpoint) in pieces of 16 (8) bytes, piece-major, so that neighbouring
 // threads touch neighbouring pieces.
@@ -502,9 +532,10 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
     }
     if constexpr (sizeof(TX) == 1) {
       const uint2 v = *reinterpret_cast<const uint2*>(x + i * T * 8);
+      bytes_to_float(v.x, xh);
+      bytes_to_float(v.y, xh + 4);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        xh[j] = __fmul_rn((float)(int8_t)(((j < 4 ? v.x : v.y) >> (8 * (j & 3))) & 255u), xs);
+      for (int j = 0; j < 8; ++j) xh[j] = __fmul_rn(xh[j], xs);
     } else {
       Raw8<TX> r;
 #pragma unroll
@@ -517,15 +548,25 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
 
   int stage = 0, buf = 0;
   const float inv_k = 1.0f / (float)p.K;
-  for (int64_t m = first; m < p.M; m += step) {
-    const float rstd = __ldg(p.rstd + m);
-    float mean = 0.f, xs[NU];
-    if constexpr (sizeof(TX) > 1) mean = __ldg(p.mean + m);
+  // The next row's scalars are on the way while a row is worked on.
+  float rstd_n = 0.f, mean_n = 0.f, xs_n[NU];
+  auto scalars = [&](int64_t m) {
+    if (m >= p.M) return;
+    rstd_n = __ldg(p.rstd + m);
+    if constexpr (sizeof(TX) > 1) mean_n = __ldg(p.mean + m);
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      xs[i] = 0.f;
-      if (sizeof(TX) == 1 && g.tid + i * T < units) xs[i] = __ldg(p.xs + (m * units + g.tid + i * T) / 8);
-    }
+    for (int i = 0; i < NU; ++i)
+      if (sizeof(TX) == 1 && g.tid + i * T < units) xs_n[i] = __ldg(p.xs + (m * units + g.tid + i * T) / 8);
+  };
+#pragma unroll
+  for (int i = 0; i < NU; ++i) xs_n[i] = 0.f;
+  scalars(first);
+  for (int64_t m = first; m < p.M; m += step) {
+    const float rstd = rstd_n, mean = mean_n;
+    float xs[NU];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) xs[i] = xs_n[i];
+    scalars(m + step);
     // The stage read last is this thread's own, and read.
     request();
     if (stages == 4)
@@ -552,21 +593,16 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
         }
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
+    pair_sum(a, b);
     if (T > 32) {
       float2* mine = red[buf] + (g.id * T >> 5);
       if ((threadIdx.x & 31) == 0) mine[g.tid >> 5] = make_float2(a, b);
       g.sync();  // one barrier per row: the buffers alternate
-      a = b = 0.f;
-      for (int k = 0; k < g.warps; ++k) {
-        const float2 v = mine[k];
-        a += v.x;
-        b += v.y;
-      }
+      const int l = threadIdx.x & 31;
+      const float2 v = l < g.warps ? mine[l] : make_float2(0.f, 0.f);
+      a = v.x;
+      b = v.y;
+      pair_sum(a, b);
       buf ^= 1;
     }
     a *= inv_k;
@@ -680,26 +716,30 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_grad_long_kernel(const
   }
 }
 
-// dw and db from the CTAs' shares: 32 columns per CTA, eight threads per column
-// take every eighth share each, in order.
-__global__ void __launch_bounds__(256)
+// dw and db from the CTAs' shares: 32 columns per CTA, 32 threads per column
+// take every 32nd share each, and add up in order.
+__global__ void __launch_bounds__(1024)
 norm_colsum_kernel(const float* __restrict__ part, int parts, int64_t K, float* __restrict__ dw,
                    float* __restrict__ db) {
-  __shared__ float red[8][32];
-  const int64_t c = blockIdx.x * (int64_t)32 + (threadIdx.x & 31);  // 0 .. 2K: a multiple of 32
-  const int k = threadIdx.x >> 5;
-  float s = 0.f;
-#pragma unroll 4
-  for (int i = k; i < parts; i += 8) s += __ldg(part + (int64_t)i * 2 * K + c);
-  red[k][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (k != 0) return;
+  __shared__ float red[32][33];
+  const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const int64_t c = blockIdx.x * (int64_t)32;  // of 0 .. 2K, a multiple of 64
+  pdl_wait_prior_grid();
+  float v[(kNormGradParts + 31) / 32];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) s += red[i][threadIdx.x];
-  if (c < K)
-    dw[c] = s;
+  for (int i = 0; i < (kNormGradParts + 31) / 32; ++i)
+    v[i] = k + 32 * i < parts ? __ldg(part + (int64_t)(k + 32 * i) * 2 * K + c + lane) : 0.f;
+  float s = v[0];
+#pragma unroll
+  for (int i = 1; i < (kNormGradParts + 31) / 32; ++i) s += v[i];
+  red[k][lane] = s;
+  __syncthreads();
+  s = warp_sum_f(red[lane][k]);  // warp k has column k now
+  if (lane != 0) return;
+  if (c + k < K)
+    dw[c + k] = s;
   else if (db != nullptr)
-    db[c - K] = s;
+    db[c + k - K] = s;
 }
 
 // ---------------------------------------------------------------------------

@@ -538,15 +538,29 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // contiguous bytes per row and a group's lanes are neighbours.
 
 // Round(w ÷ s) to the nearest integer, ties to even, as for the exact
-// quotient: w is near k·s, both k·s (4 + 8 bits) and the residual w − k·s
-// are exact in fp32, so the residual against s/2 settles what the rounding
-// of the fp32 quotient may have moved onto or over a border.
-__device__ __forceinline__ float w4_round_quotient(float w, float s) {
-  float k = rintf(__fdiv_rn(w, s));
-  const float r = fmaf(-k, s, w), h = 0.5f * s, dir = copysignf(1.0f, r);
-  if (fabsf(r) > h || (fabsf(r) == h && fmodf(k, 2.0f) != 0.0f)) k += dir;
-  return k;
-}
+// quotient, |w| < 16·s. The product with a rounded 1/s is near enough to be off
+// by one at most; the residual w − k·s is exact in fp32 (k·s has 5 + 8 bits), so
+// it says against s/2 whether k is the nearest. s below 2^-60 comes scaled.
+struct W4Rounder {
+  float s, half, inv, up;
+  __device__ __forceinline__ explicit W4Rounder(float scale) {
+    up = scale < 0x1p-60f ? 0x1p80f : 1.0f;  // exact, and 1/s stays finite
+    s = scale * up;
+    half = 0.5f * s;
+    inv = s > 0.f ? __fdividef(1.0f, s) : 0.f;
+  }
+  __device__ __forceinline__ float operator()(float w) const {
+    w *= up;
+    float k = __fadd_rn(__fmul_rn(w, inv), 12582912.0f) - 12582912.0f;
+    const float r = fmaf(-k, s, w);
+    if (fabsf(r) >= half) {  // off by one, or a tie
+      const float dir = copysignf(1.0f, r);
+      const bool odd = ((int)k & 1) != 0;
+      if (fabsf(r) > half || (odd && s > 0.f)) k += dir;
+    }
+    return k;
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void w4_load8(const T* p, float (&v)[8]) {
@@ -609,13 +623,14 @@ w4_quant_kernel(const T* __restrict__ W, int64_t N, int64_t K, int G, uint32_t* 
                                        : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
     const __nv_bfloat16 sb = __float2bfloat16_rn(raw);
     const float s = __bfloat162float(sb);
+    const W4Rounder round(s);
     float z = 8.0f;
-    if (zeros != nullptr) z = s > 0.f ? fminf(w4_round_quotient(-lo, s), 15.0f) : 0.0f;
+    if (zeros != nullptr) z = s > 0.f ? fminf(round(-lo), 15.0f) : 0.0f;
     uint32_t q[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float c = s > 0.f ? w4_round_quotient(v[j], s) + z : z;
-      q[j] = (uint32_t)fminf(fmaxf(c, 0.0f), 15.0f);
+      const float c = s > 0.f ? fminf(fmaxf(round(v[j]) + z, 0.0f), 15.0f) : z;
+      q[j] = __float_as_uint(c + 8388608.0f) & 15u;
     }
     W4[w4_word_index(blk, r, l)] = w4_word(q);
     if (l % gl == 0) {
