@@ -949,55 +949,72 @@ bl_status launch_w4(const W4Params& p, int group, bool pdl, int dev, int sms, cu
 
 // --------------------------------------------------------------------------
 // Layer norm and 8-bit checkpoints.
-// Units of eight columns per thread and threads per row: few units while the
-// row fits 512 threads.
+#ifndef NORMTHREADS
+#define NORMTHREADS 640
+#endif
+// Units of eight columns per thread and threads per row: four with many rows
+// (what the threads of a row exchange costs more than their columns do), as
+// few as 512 threads allow with few.
 struct NormShape {
   int nu, group;  // nu 0: the row is too long for registers
 };
-NormShape norm_shape(int64_t K) {
+NormShape norm_shape(int64_t M, int64_t K, int sms) {
   const int64_t units = K / 8;
-  const int nu = units <= 128 ? 1 : units <= 1024 ? 2 : units <= 2048 ? 4 : 0;
-  if (nu == 0) return {0, 0};
-  return {nu, (int)((((units + nu - 1) / nu) + 31) / 32 * 32)};
+  for (int nu = M >= 2 * sms ? 4 : 1; nu <= 4; nu *= 2) {
+    const int64_t group = ((units + nu - 1) / nu + 31) / 32 * 32;
+    if (group > kNormMaxThreads) continue;
+    int need = 1;  // no more units than such a group needs
+    while (need * group < units) need *= 2;
+    return {need, (int)group};
+  }
+  return {0, 0};
 }
 
+template <typename T, typename OUT, int NU>
+bl_status launch_norm_nu(const NormParams& p, int group, int sms, cudaStream_t st) {
+  const int groups = group >= 128 ? 1 : 128 / group;  // at least 128 threads to a CTA
+  const int threads = groups * group, per_sm = NORMTHREADS / threads < 1 ? 1 : NORMTHREADS / threads;
+  int64_t grid = (p.M + groups - 1) / groups;
+  if (grid > (int64_t)per_sm * sms) grid = (int64_t)per_sm * sms;
+  if (p.K / 8 == (int64_t)group * NU)
+    layernorm_kernel<T, OUT, NU, true><<<(unsigned)grid, threads, 0, st>>>(p, group);
+  else
+    layernorm_kernel<T, OUT, NU, false><<<(unsigned)grid, threads, 0, st>>>(p, group);
+  BL_CUDA(cudaGetLastError());
+  return BL_OK;
+}
 template <typename T, typename OUT>
-bl_status launch_norm_out(const NormParams& p, cudaStream_t st) {
-  const NormShape s = norm_shape(p.K);
-  if (s.nu == 0) {
-    layernorm_long_kernel<T, OUT><<<(unsigned)p.M, kNormThreads, 0, st>>>(p);
-  } else {
-    const int groups = s.group >= 128 ? 1 : 128 / s.group;  // at least 128 threads to a CTA
-    const dim3 grid((unsigned)((p.M + groups - 1) / groups)), block(groups * s.group);
-    if (s.nu == 1)
-      layernorm_kernel<T, OUT, 1><<<grid, block, 0, st>>>(p, s.group);
-    else if (s.nu == 2)
-      layernorm_kernel<T, OUT, 2><<<grid, block, 0, st>>>(p, s.group);
-    else
-      layernorm_kernel<T, OUT, 4><<<grid, block, 0, st>>>(p, s.group);
-  }
+bl_status launch_norm_out(const NormParams& p, int sms, cudaStream_t st) {
+  const NormShape s = norm_shape(p.M, p.K, sms);
+  if (s.nu == 1) return launch_norm_nu<T, OUT, 1>(p, s.group, sms, st);
+  if (s.nu == 2) return launch_norm_nu<T, OUT, 2>(p, s.group, sms, st);
+  if (s.nu == 4) return launch_norm_nu<T, OUT, 4>(p, s.group, sms, st);
+  layernorm_long_kernel<T, OUT><<<(unsigned)p.M, kNormThreads, 0, st>>>(p);
   BL_CUDA(cudaGetLastError());
   return BL_OK;
 }
 template <typename T>
-bl_status launch_norm(const NormParams& p, int out, cudaStream_t st) {
-  if (out == 0) return launch_norm_out<T, float>(p, st);
-  if (out == 1) return launch_norm_out<T, __nv_bfloat16>(p, st);
-  return launch_norm_out<T, int8_t>(p, st);
+bl_status launch_norm(const NormParams& p, int out, int sms, cudaStream_t st) {
+  if (out == 0) return launch_norm_out<T, float>(p, sms, st);
+  if (out == 1) return launch_norm_out<T, __nv_bfloat16>(p, sms, st);
+  return launch_norm_out<T, int8_t>(p, sms, st);
 }
 
 inline int64_t norm_grad_parts(int64_t M) { return M < kNormGradParts ? M : kNormGradParts; }
 
 template <typename TD, typename TX, typename TO, int NU>
 bl_status launch_norm_grad_nu(const NormGradParams& p, int grid, int dev, cudaStream_t st) {
-  const int64_t units = p.K / 8;
+  const int64_t units = p.K / 4;
   const int group = (int)(((units + NU - 1) / NU + 31) / 32 * 32);
-  int groups = (NU == 1 ? 1024 : 512) / group;
+  int groups = kNormGradThreads<NU> / group;
   if (groups > 15 && group > 32) groups = 15;  // a named barrier each
   const int64_t rows = (p.M + grid - 1) / grid;
   if (groups > rows) groups = (int)rows;
-  const int stage = norm_stage_bytes<TD, TX, NU>(group) * groups;
-  const int stages = stage * 4 <= 200 * 1024 ? 4 : stage * 3 <= 200 * 1024 ? 3 : 2;
+  // Rows in flight: at least three ring stages if fewer groups allow them.
+  const int cap = 224 * 1024, row = norm_stage_bytes<TD, TX, NU>(group);
+  while (groups > 1 && 3 * row * groups > cap) --groups;
+  const int stage = row * groups;
+  const int stages = stage * 4 <= cap ? 4 : stage * 3 <= cap ? 3 : 2;
   size_t smem = (size_t)stage * stages;
   const size_t share = (size_t)groups * 2 * p.K * 4;
   if (smem < share) smem = share;
@@ -1010,11 +1027,11 @@ bl_status launch_norm_grad_nu(const NormGradParams& p, int grid, int dev, cudaSt
 
 template <typename TD, typename TX, typename TO>
 bl_status launch_norm_grad_out(const NormGradParams& p, int grid, int dev, cudaStream_t st) {
-  if (p.K <= 1024) return launch_norm_grad_nu<TD, TX, TO, 1>(p, grid, dev, st);
-  if (p.K <= 8192) return launch_norm_grad_nu<TD, TX, TO, 2>(p, grid, dev, st);
+  if (p.K <= 1024) return launch_norm_grad_nu<TD, TX, TO, 2>(p, grid, dev, st);
+  if (p.K <= 8192) return launch_norm_grad_nu<TD, TX, TO, 4>(p, grid, dev, st);
   // two ring stages of the row have to fit in shared memory
-  if (p.K <= 16384 && 2 * norm_stage_bytes<TD, TX, 4>((int)((p.K / 32 + 31) / 32 * 32)) <= 226 * 1024)
-    return launch_norm_grad_nu<TD, TX, TO, 4>(p, grid, dev, st);
+  if (p.K <= 16384 && 2 * norm_stage_bytes<TD, TX, 8>((int)((p.K / 32 + 31) / 32 * 32)) <= 224 * 1024)
+    return launch_norm_grad_nu<TD, TX, TO, 8>(p, grid, dev, st);
   layernorm_grad_long_kernel<TD, TX, TO><<<grid, kNormThreads, 0, st>>>(p);
   BL_CUDA(cudaGetLastError());
   return BL_OK;
@@ -2096,7 +2113,7 @@ bl_status bl_layernorm(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, co
   p.rstd = rstd;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int out = y_dtype == BL_BF16 ? 1 : 0;
-  return x_dtype == BL_BF16 ? launch_norm<__nv_bfloat16>(p, out, st) : launch_norm<float>(p, out, st);
+  return x_dtype == BL_BF16 ? launch_norm<__nv_bfloat16>(p, out, sms, st) : launch_norm<float>(p, out, sms, st);
 }
 
 bl_status bl_layernorm_quant(const void* X, bl_dtype x_dtype, int64_t M, int64_t K,
@@ -2139,7 +2156,7 @@ bl_status bl_layernorm_quant(const void* X, bl_dtype x_dtype, int64_t M, int64_t
   p.xq = xhat_q;
   p.xs = xhat_scale;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return x_dtype == BL_BF16 ? launch_norm<__nv_bfloat16>(p, 2, st) : launch_norm<float>(p, 2, st);
+  return x_dtype == BL_BF16 ? launch_norm<__nv_bfloat16>(p, 2, sms, st) : launch_norm<float>(p, 2, sms, st);
 }
 
 size_t bl_layernorm_grad_workspace_bytes(int64_t M, int64_t K) {

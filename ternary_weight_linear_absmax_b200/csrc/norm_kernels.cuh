@@ -44,6 +44,11 @@ __device__ __forceinline__ void norm_load8(const T* p, float (&v)[8]) {
   }
 }
 
+__device__ __forceinline__ void norm_load4(const float* p, float (&v)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+
 template <typename T>
 __device__ __forceinline__ void norm_store8(T* p, const float (&v)[8]) {
   if constexpr (sizeof(T) == 2) {
@@ -58,6 +63,48 @@ __device__ __forceinline__ void norm_store8(T* p, const float (&v)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
   }
+}
+
+// A unit of eight columns as a thread takes it: four and, 32 further on, four
+// more of a group of 64, which eight neighbouring threads share. So a warp's
+// accesses fill whole sectors whatever the type. `c` is the unit's first column.
+__device__ __forceinline__ int64_t unit_column(int64_t u) { return (u >> 3) * 64 + (u & 7) * 4; }
+template <typename T>
+__device__ __forceinline__ void load_unit(const T* row, int64_t c, float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(row + c + 32 * h));
+      v[4 * h] = a.x; v[4 * h + 1] = a.y; v[4 * h + 2] = a.z; v[4 * h + 3] = a.w;
+    } else {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(row + c + 32 * h));
+      v[4 * h] = __uint_as_float(a.x << 16);
+      v[4 * h + 1] = __uint_as_float(a.x & 0xFFFF0000u);
+      v[4 * h + 2] = __uint_as_float(a.y << 16);
+      v[4 * h + 3] = __uint_as_float(a.y & 0xFFFF0000u);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_unit(T* row, int64_t c, const float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(row + c + 32 * h) =
+          make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v[4 * h], v[4 * h + 1]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[4 * h + 2], v[4 * h + 3]);
+      *reinterpret_cast<uint2*>(row + c + 32 * h) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+  }
+}
+// Eight bytes of a unit, four per word.
+__device__ __forceinline__ void store_unit_bytes(void* row, int64_t c, uint32_t w0, uint32_t w1) {
+  uint8_t* p = reinterpret_cast<uint8_t*>(row) + c;
+  *reinterpret_cast<uint32_t*>(p) = w0;
+  *reinterpret_cast<uint32_t*>(p + 32) = w1;
 }
 
 __device__ __forceinline__ float warp_sum_f(float v) {
@@ -137,18 +184,19 @@ struct NormParams {
   float* xs;            // [M, K/64]
 };
 
-__device__ __forceinline__ void norm_affine8(const float (&x)[8], float mean, float rstd,
-                                             const float* weight, const float* bias, int64_t c,
-                                             float (&xhat)[8], float (&y)[8]) {
+// x̂ and y of a unit from d = x − μ; y may be d.
+__device__ __forceinline__ void norm_affine_unit(const float (&d)[8], float rstd, const float* weight,
+                                                 const float* bias, int64_t c, float (&xhat)[8],
+                                                 float (&y)[8]) {
   float w[8];
-  norm_load8(weight + c, w);
+  load_unit(weight, c, w);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    xhat[j] = __fmul_rn(__fsub_rn(x[j], mean), rstd);
+    xhat[j] = __fmul_rn(d[j], rstd);
     y[j] = __fmul_rn(xhat[j], w[j]);
   }
   if (bias != nullptr) {
-    norm_load8(bias + c, w);
+    load_unit(bias, c, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = __fadd_rn(y[j], w[j]);
   }
@@ -194,132 +242,147 @@ __device__ __forceinline__ float rsqrt_once(double v) {
   return (float)r;
 }
 
-// Eight raw elements of a row, as loaded.
+// A unit as loaded.
 template <typename T>
-struct Raw8 {
-  uint4 a[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p) {
+struct RawUnit {
+  uint2 a[sizeof(T)];
+  __device__ __forceinline__ void load(const T* row, int64_t c) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) a[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      for (int h = 0; h < 2; ++h) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + c + 32 * h));
+        a[2 * h] = make_uint2(q.x, q.y);
+        a[2 * h + 1] = make_uint2(q.z, q.w);
+      }
+    } else {
+      a[0] = __ldg(reinterpret_cast<const uint2*>(row + c));
+      a[1] = __ldg(reinterpret_cast<const uint2*>(row + c + 32));
+    }
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-      const uint32_t w[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (sizeof(T) == 2) {
-          v[2 * j] = __uint_as_float(w[j] << 16);
-          v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        } else {
-          v[4 * i + j] = __uint_as_float(w[j]);
-        }
+    for (int i = 0; i < (int)sizeof(T); ++i) {
+      if constexpr (sizeof(T) == 4) {
+        v[2 * i] = __uint_as_float(a[i].x);
+        v[2 * i + 1] = __uint_as_float(a[i].y);
+      } else {
+        v[4 * i] = __uint_as_float(a[i].x << 16);
+        v[4 * i + 1] = __uint_as_float(a[i].x & 0xFFFF0000u);
+        v[4 * i + 2] = __uint_as_float(a[i].y << 16);
+        v[4 * i + 3] = __uint_as_float(a[i].y & 0xFFFF0000u);
       }
     }
   }
 };
 
-// One row per group of T threads, NU units of eight columns per thread, the
-// row in registers between the passes. OUT: fp32/bf16 rows, or int8_t for the
-// tokens.
-template <typename T, typename OUT, int NU>
+// One row per group of T threads at a time, NU units of eight columns per
+// thread, the row in registers between the passes and the next one on its way.
+// FULL: the units are T·NU, every thread has all of its own. OUT: fp32/bf16
+// rows, or int8_t for the tokens.
+template <typename T, typename OUT, int NU, bool FULL>
 __global__ void __launch_bounds__(kNormMaxThreads) layernorm_kernel(const NormParams p, int group) {
   __shared__ double redd[2][32];
   __shared__ float redf[32];
   __shared__ int redi[32];
   const RowGroup g(group);
-  const int64_t m = (int64_t)blockIdx.x * (blockDim.x / group) + g.id;
-  if (m >= p.M) return;  // whole groups
-  const int units = (int)(p.K / 8);
-  const T* row = reinterpret_cast<const T*>(p.X) + m * p.K;
-  Raw8<T> raw[NU];
-#pragma unroll
-  for (int i = 0; i < NU; ++i) {
-    const int u = g.tid + i * g.T;
-    if (u < units) raw[i].load(row + 8 * u);
-  }
-  float x[8];
-  double s = 0.0;
-#pragma unroll
-  for (int i = 0; i < NU; ++i) {
-    if (g.tid + i * g.T < units) {
-      raw[i].get(x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s += (double)x[j];
-    }
-  }
+  const int units = (int)(p.K / 8), groups = (int)blockDim.x / group;
+  const int64_t step = (int64_t)gridDim.x * groups;
   auto add = [](auto a, auto b) { return a + b; };
-  const float mean = (float)(group_reduce(g, s, redd[0], add) * p.inv_k);
-  s = 0.0;
+  auto has = [&](int i) { return FULL || g.tid + i * g.T < units; };
+  RawUnit<T> raw[NU];
+  auto load = [&](int64_t m) {
+    if (m >= p.M) return;
+    const T* row = reinterpret_cast<const T*>(p.X) + m * p.K;
 #pragma unroll
-  for (int i = 0; i < NU; ++i) {
-    if (g.tid + i * g.T < units) {
-      raw[i].get(x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const double d = (double)__fsub_rn(x[j], mean);
-        s = fma(d, d, s);
-      }
-    }
-  }
-  const float rstd = rsqrt_once(fma(group_reduce(g, s, redd[1], add), p.inv_k, (double)p.eps));
-  if (g.tid == 0) {
-    if (p.mean != nullptr) p.mean[m] = mean;
-    if (p.rstd != nullptr) p.rstd[m] = rstd;
-  }
-  float xhat[8], y[8];
-  if constexpr (sizeof(OUT) > 1) {
+    for (int i = 0; i < NU; ++i)
+      if (has(i)) raw[i].load(row, unit_column(g.tid + i * g.T));
+  };
+  int64_t m = (int64_t)blockIdx.x * groups + g.id;
+  load(m);
+  // The barriers in between keep a buffer from being written for the next row
+  // while a warp still reads it.
+  for (; m < p.M; m += step) {
+    float v[NU][8];
+    double s[4] = {0.0, 0.0, 0.0, 0.0};  // four chains: a 64-bit addition takes long
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const int u = g.tid + i * g.T;
-      if (u < units) {
-        raw[i].get(x);
-        norm_affine8(x, mean, rstd, p.weight, p.bias, 8 * u, xhat, y);
-        norm_store8(reinterpret_cast<OUT*>(p.Y) + m * p.K + 8 * u, y);
+      if (has(i)) {
+        raw[i].get(v[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j & 3] += (double)v[i][j];
       }
     }
-  } else {
-    float mx = 0.f, keep[NU][8];
+    load(m + step);
+    const float mean = (float)(group_reduce(g, (s[0] + s[1]) + (s[2] + s[3]), redd[0], add) * p.inv_k);
+    s[0] = s[1] = s[2] = s[3] = 0.0;
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {  // whole warps: a checkpoint group is eight lanes
-      const int u = g.tid + i * g.T;
+    for (int i = 0; i < NU; ++i) {
+      if (has(i)) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) xhat[j] = 0.f;
-      if (u < units) {
-        raw[i].get(x);
-        norm_affine8(x, mean, rstd, p.weight, p.bias, 8 * u, xhat, keep[i]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(keep[i][j]));
-      }
-      if (p.xq != nullptr) {
-        uint32_t w0, w1;
-        const float sc = ckpt_codes8<true>(xhat, w0, w1);
-        if (u < units) {
-          *reinterpret_cast<uint2*>(p.xq + m * p.K + 8 * u) = make_uint2(w0, w1);
-          if ((u & 7) == 0) p.xs[(m * p.K + 8 * u) / 64] = sc;
+        for (int j = 0; j < 8; ++j) {
+          v[i][j] = __fsub_rn(v[i][j], mean);
+          const double d = (double)v[i][j];
+          s[j & 3] = fma(d, d, s[j & 3]);
         }
       }
     }
-    mx = group_reduce(g, mx, redf, [](float a, float b) { return fmaxf(a, b); });
-    const float scale = __fdiv_rn(127.0f, __fadd_rn(mx, p.q_eps));
-    int sum = 0;
-#pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      const int u = g.tid + i * g.T;
-      if (u < units) {
-        uint32_t b[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = quant_i8_bits(keep[i][j], scale);
-        const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
-        const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
-        sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
-        *reinterpret_cast<uint2*>(p.Aq + m * p.K + 8 * u) = make_uint2(w0, w1);
-      }
-    }
-    if (p.rowsum != nullptr) sum = group_reduce(g, sum, redi, add);
+    const float rstd = rsqrt_once(
+        fma(group_reduce(g, (s[0] + s[1]) + (s[2] + s[3]), redd[1], add), p.inv_k, (double)p.eps));
     if (g.tid == 0) {
-      p.gamma[m] = mx;
-      if (p.rowsum != nullptr) p.rowsum[m] = sum;
+      if (p.mean != nullptr) p.mean[m] = mean;
+      if (p.rstd != nullptr) p.rstd[m] = rstd;
+    }
+    float xhat[8];
+    if constexpr (sizeof(OUT) > 1) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        if (has(i)) {
+          const int64_t c = unit_column(g.tid + i * g.T);
+          norm_affine_unit(v[i], rstd, p.weight, p.bias, c, xhat, v[i]);
+          store_unit(reinterpret_cast<OUT*>(p.Y) + m * p.K, c, v[i]);
+        }
+      }
+    } else {
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {  // whole warps: a checkpoint group is eight lanes
+        const int u = g.tid + i * g.T;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) xhat[j] = 0.f;
+        if (has(i)) {
+          norm_affine_unit(v[i], rstd, p.weight, p.bias, unit_column(u), xhat, v[i]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[i][j]));
+        }
+        if (p.xq != nullptr) {
+          uint32_t w0, w1;
+          const float sc = ckpt_codes8<true>(xhat, w0, w1);
+          if (has(i)) {
+            store_unit_bytes(p.xq + m * p.K, unit_column(u), w0, w1);
+            if ((u & 7) == 0) p.xs[(m * p.K + 8 * u) / 64] = sc;
+          }
+        }
+      }
+      mx = group_reduce(g, mx, redf, [](float a, float b) { return fmaxf(a, b); });
+      const float scale = __fdiv_rn(127.0f, __fadd_rn(mx, p.q_eps));
+      int sum = 0;
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        if (has(i)) {
+          uint32_t b[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) b[j] = quant_i8_bits(v[i][j], scale);
+          const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
+          const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
+          sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
+          store_unit_bytes(p.Aq + m * p.K, unit_column(g.tid + i * g.T), w0, w1);
+        }
+      }
+      if (p.rowsum != nullptr) sum = group_reduce(g, sum, redi, add);
+      if (g.tid == 0) {
+        p.gamma[m] = mx;
+        if (p.rowsum != nullptr) p.rowsum[m] = sum;
+      }
     }
   }
 }
@@ -334,14 +397,14 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
   float x[8];
   double s = 0.0;
   for (int64_t u = threadIdx.x; u < units; u += kNormThreads) {
-    norm_load8(row + 8 * u, x);
+    load_unit(row, unit_column(u), x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) s += (double)x[j];
   }
   const float mean = (float)(block_sum_d(s, redd) * p.inv_k);
   s = 0.0;
   for (int64_t u = threadIdx.x; u < units; u += kNormThreads) {
-    norm_load8(row + 8 * u, x);
+    load_unit(row, unit_column(u), x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const double d = (double)__fsub_rn(x[j], mean);
@@ -356,9 +419,10 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
   float xhat[8], y[8];
   if constexpr (sizeof(OUT) > 1) {
     for (int64_t u = threadIdx.x; u < units; u += kNormThreads) {
-      norm_load8(row + 8 * u, x);
-      norm_affine8(x, mean, rstd, p.weight, p.bias, 8 * u, xhat, y);
-      norm_store8(reinterpret_cast<OUT*>(p.Y) + m * p.K + 8 * u, y);
+      load_unit(row, unit_column(u), x);
+      for (int j = 0; j < 8; ++j) x[j] = __fsub_rn(x[j], mean);
+      norm_affine_unit(x, rstd, p.weight, p.bias, unit_column(u), xhat, y);
+      store_unit(reinterpret_cast<OUT*>(p.Y) + m * p.K, unit_column(u), y);
     }
   } else {
     float mx = 0.f;
@@ -368,8 +432,9 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
 #pragma unroll
       for (int j = 0; j < 8; ++j) xhat[j] = 0.f;
       if (u < units) {
-        norm_load8(row + 8 * u, x);
-        norm_affine8(x, mean, rstd, p.weight, p.bias, 8 * u, xhat, y);
+        load_unit(row, unit_column(u), x);
+        for (int j = 0; j < 8; ++j) x[j] = __fsub_rn(x[j], mean);
+      norm_affine_unit(x, rstd, p.weight, p.bias, unit_column(u), xhat, y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(y[j]));
       }
@@ -377,7 +442,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
         uint32_t w0, w1;
         const float sc = ckpt_codes8<true>(xhat, w0, w1);
         if (u < units) {
-          *reinterpret_cast<uint2*>(p.xq + m * p.K + 8 * u) = make_uint2(w0, w1);
+          store_unit_bytes(p.xq + m * p.K, unit_column(u), w0, w1);
           if ((u & 7) == 0) p.xs[(m * p.K + 8 * u) / 64] = sc;
         }
       }
@@ -386,15 +451,16 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
     const float scale = __fdiv_rn(127.0f, __fadd_rn(mx, p.q_eps));
     int sum = 0;
     for (int64_t u = threadIdx.x; u < units; u += kNormThreads) {
-      norm_load8(row + 8 * u, x);
-      norm_affine8(x, mean, rstd, p.weight, p.bias, 8 * u, xhat, y);
+      load_unit(row, unit_column(u), x);
+      for (int j = 0; j < 8; ++j) x[j] = __fsub_rn(x[j], mean);
+      norm_affine_unit(x, rstd, p.weight, p.bias, unit_column(u), xhat, y);
       uint32_t b[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) b[j] = quant_i8_bits(y[j], scale);
       const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
       const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
       sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
-      *reinterpret_cast<uint2*>(p.Aq + m * p.K + 8 * u) = make_uint2(w0, w1);
+      store_unit_bytes(p.Aq + m * p.K, unit_column(u), w0, w1);
     }
     __shared__ int redi[kNormThreads / 32];
     sum = warp_sum_i(sum);
@@ -429,11 +495,50 @@ struct NormGradParams {
   float* part;         // [grid, 2, K]
 };
 
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes) {
-  if (bytes == 16)
+// Four signed bytes as floats: byte ^ 0x80 in the low bits of 2^23.
+__device__ __forceinline__ void bytes_to_float(uint32_t w, float* v) {
+  w ^= 0x80808080u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 | j)) - 8388736.0f;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
+// Four elements from shared memory as fp32.
+template <typename T>
+__device__ __forceinline__ void lds4(uint32_t a, float (&v)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(a));
+  } else if constexpr (sizeof(T) == 2) {
+    uint32_t x, y;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(a));
+    v[0] = __uint_as_float(x << 16);
+    v[1] = __uint_as_float(x & 0xFFFF0000u);
+    v[2] = __uint_as_float(y << 16);
+    v[3] = __uint_as_float(y & 0xFFFF0000u);
+  } else {
+    uint32_t w;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(a));
+    bytes_to_float(w, v);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float (&v)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
 }
 
 // Sums of a and b over the warp, returned to all lanes. The first step leaves
@@ -448,58 +553,47 @@ __device__ __forceinline__ void pair_sum(float& a, float& b) {
   b = __shfl_sync(0xffffffffu, v, 16);
 }
 
-// Four signed bytes as floats: byte ^ 0x80 in the low bits of 2^23.
-__device__ __forceinline__ void bytes_to_float(uint32_t w, float* v) {
-  w ^= 0x80808080u;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    v[j] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 | j)) - 8388736.0f;
-}
+// Threads of a CTA at most: 12·NU registers hold dw, db and w, 8·NU the row.
+template <int NU>
+constexpr int kNormGradThreads = 512;
 
-// Bytes of one row in a ring stage, for one group of T threads: dY and X (or
-// the checkpoint) in pieces of 16 (8) bytes, piece-major, so that neighbouring
-// threads touch neighbouring pieces.
+// Bytes of one row in a ring stage, for one group of T threads: pieces of four
+// elements, neighbouring threads on neighbouring pieces (whole sectors).
 template <typename TD, typename TX, int NU>
 __host__ __device__ constexpr int norm_stage_bytes(int T) {
-  return NU * T * 8 * (int)(sizeof(TD) + sizeof(TX));
+  return NU * T * 4 * (int)(sizeof(TD) + sizeof(TX));
 }
 
-// One row per group of T threads at a time, NU units of eight columns per
+// One row per group of T threads at a time, NU units of four columns per
 // thread. A thread copies its own columns of the coming rows into its part of
 // the ring (cp.async: nobody else reads them, so no barrier guards the ring),
 // and keeps their shares of dw and db in registers; the two row sums are the
 // only thing that the group exchanges. The CTA's groups add up their shares in
 // shared memory at the end.
 template <typename TD, typename TX, typename TO, int NU>
-__global__ void __launch_bounds__(NU == 1 ? 1024 : 512)
+__global__ void __launch_bounds__(kNormGradThreads<NU>)
 layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 red[2][32];
   const RowGroup g(group);
-  const int groups = (int)blockDim.x / group, T = group, units = (int)(p.K / 8);
-  constexpr int PD = sizeof(TD) / 2;                      // 16-byte pieces of a unit of dY
-  constexpr int PX = sizeof(TX) == 1 ? 1 : sizeof(TX) / 2, XB = sizeof(TX) == 1 ? 8 : 16;
+  const int groups = (int)blockDim.x / group, T = group, units = (int)(p.K / 4);
+  constexpr int BD = 4 * sizeof(TD), BX = 4 * sizeof(TX);  // bytes of a piece
   const int stage_bytes = norm_stage_bytes<TD, TX, NU>(T);
   const uint32_t ring = smem_u32(smem) + g.id * stages * stage_bytes;
-  const uint32_t mine_d = ring + 16 * g.tid, mine_x = ring + NU * T * 16 * PD + XB * g.tid;
+  const uint32_t mine_d = ring + BD * g.tid, mine_x = ring + NU * T * BD + BX * g.tid;
   const int64_t step = (int64_t)gridDim.x * groups;
   int64_t next = (int64_t)g.id * gridDim.x + blockIdx.x;  // the next row to request
   const int64_t first = next;
   int q = 0;
   auto request = [&]() {
     if (next < p.M) {
+      const TD* d = reinterpret_cast<const TD*>(p.dY) + next * p.K + 4 * g.tid;
+      const TX* x = reinterpret_cast<const TX*>(p.X) + next * p.K + 4 * g.tid;
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
-        const int u = g.tid + i * T;
-        if (u < units) {
-          const uint8_t* d = reinterpret_cast<const uint8_t*>(p.dY) + (next * p.K + 8 * u) * (int64_t)sizeof(TD);
-          const uint8_t* x = reinterpret_cast<const uint8_t*>(p.X) + (next * p.K + 8 * u) * (int64_t)sizeof(TX);
-#pragma unroll
-          for (int c = 0; c < PD; ++c)
-            cp_async(mine_d + q * stage_bytes + (i * PD + c) * T * 16, d + 16 * c, 16);
-#pragma unroll
-          for (int c = 0; c < PX; ++c)
-            cp_async(mine_x + q * stage_bytes + (i * PX + c) * T * XB, x + 16 * c, XB);
+        if (g.tid + i * T < units) {
+          cp_async<BD>(mine_d + q * stage_bytes + i * T * BD, d + 4 * i * T);
+          cp_async<BX>(mine_x + q * stage_bytes + i * T * BX, x + 4 * i * T);
         }
       }
     }
@@ -509,41 +603,20 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
   };
   for (int s = 0; s < stages - 1; ++s) request();
 
-  float dw[NU][8], db[NU][8], w[NU][8];
+  float dw[NU][4], db[NU][4], w[NU][4];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int u = g.tid + i * T;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = w[i][j] = 0.f;
-    if (NU < 4 && u < units) norm_load8(p.weight + 8 * u, w[i]);
+    for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = w[i][j] = 0.f;
+    if (NU < 8 && u < units) norm_load4(p.weight + 4 * u, w[i]);
   }
-  auto get = [&](int stage, int i, float mean, float rstd, float xs, float (&dy)[8], float (&xh)[8]) {
-    const uint8_t* d = smem + (mine_d - smem_u32(smem)) + stage * stage_bytes;
-    const uint8_t* x = smem + (mine_x - smem_u32(smem)) + stage * stage_bytes;
-    if constexpr (PD == 1) {
-      Raw8<__nv_bfloat16> r;
-      r.a[0] = *reinterpret_cast<const uint4*>(d + i * T * 16);
-      r.get(dy);
-    } else {
-      Raw8<float> r;
-      r.a[0] = *reinterpret_cast<const uint4*>(d + (i * 2) * T * 16);
-      r.a[1] = *reinterpret_cast<const uint4*>(d + (i * 2 + 1) * T * 16);
-      r.get(dy);
-    }
-    if constexpr (sizeof(TX) == 1) {
-      const uint2 v = *reinterpret_cast<const uint2*>(x + i * T * 8);
-      bytes_to_float(v.x, xh);
-      bytes_to_float(v.y, xh + 4);
+  auto get = [&](int stage, int i, float mean, float rstd, float xs, float (&dy)[4], float (&xh)[4]) {
+    lds4<TD>(mine_d + stage * stage_bytes + i * T * BD, dy);
+    lds4<TX>(mine_x + stage * stage_bytes + i * T * BX, xh);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) xh[j] = __fmul_rn(xh[j], xs);
-    } else {
-      Raw8<TX> r;
-#pragma unroll
-      for (int c = 0; c < PX; ++c) r.a[c] = *reinterpret_cast<const uint4*>(x + (i * PX + c) * T * 16);
-      r.get(xh);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) xh[j] = __fmul_rn(__fsub_rn(xh[j], mean), rstd);
-    }
+    for (int j = 0; j < 4; ++j)
+      xh[j] = sizeof(TX) == 1 ? __fmul_rn(xh[j], xs) : __fmul_rn(__fsub_rn(xh[j], mean), rstd);
   };
 
   int stage = 0, buf = 0;
@@ -556,7 +629,7 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
     if constexpr (sizeof(TX) > 1) mean_n = __ldg(p.mean + m);
 #pragma unroll
     for (int i = 0; i < NU; ++i)
-      if (sizeof(TX) == 1 && g.tid + i * T < units) xs_n[i] = __ldg(p.xs + (m * units + g.tid + i * T) / 8);
+      if (sizeof(TX) == 1 && g.tid + i * T < units) xs_n[i] = __ldg(p.xs + (m * units + g.tid + i * T) / 16);
   };
 #pragma unroll
   for (int i = 0; i < NU; ++i) xs_n[i] = 0.f;
@@ -575,16 +648,16 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
       asm volatile("cp.async.wait_group 2;" ::: "memory");
     else
       asm volatile("cp.async.wait_group 1;" ::: "memory");
-    float dy[NU][8], xh[NU][8];
+    float dy[NU][4], xh[NU][4];
     float a = 0.f, b = 0.f;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const int u = g.tid + i * T;
       if (u < units) {
         get(stage, i, mean, rstd, xs[i], dy[i], xh[i]);
-        if (NU == 4) norm_load8(p.weight + 8 * u, w[i]);
+        if (NU == 8) norm_load4(p.weight + 4 * u, w[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           dw[i][j] = fmaf(dy[i][j], xh[i][j], dw[i][j]);
           db[i][j] += dy[i][j];
           const float gj = dy[i][j] * w[i][j];
@@ -611,14 +684,14 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
     for (int i = 0; i < NU; ++i) {
       const int u = g.tid + i * T;
       if (u < units) {
-        if (NU == 4) {  // read again rather than kept
+        if (NU == 8) {  // read again rather than kept
           get(stage, i, mean, rstd, xs[i], dy[i], xh[i]);
-          norm_load8(p.weight + 8 * u, w[i]);
+          norm_load4(p.weight + 4 * u, w[i]);
         }
-        float dx[8];
+        float dx[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dx[j] = rstd * fmaf(-xh[i][j], b, fmaf(dy[i][j], w[i][j], -a));
-        norm_store8(reinterpret_cast<TO*>(p.dX) + m * p.K + 8 * u, dx);
+        for (int j = 0; j < 4; ++j) dx[j] = rstd * fmaf(-xh[i][j], b, fmaf(dy[i][j], w[i][j], -a));
+        store4(reinterpret_cast<TO*>(p.dX) + m * p.K + 4 * u, dx);
       }
     }
     stage = stage + 1 == stages ? 0 : stage + 1;
@@ -631,8 +704,8 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
   for (int i = 0; i < NU; ++i) {
     const int u = g.tid + i * T;
     if (u < units) {
-      norm_store8(share + (int64_t)g.id * 2 * p.K + 8 * u, dw[i]);
-      norm_store8(share + (int64_t)g.id * 2 * p.K + p.K + 8 * u, db[i]);
+      store4(share + (int64_t)g.id * 2 * p.K + 4 * u, dw[i]);
+      store4(share + (int64_t)g.id * 2 * p.K + p.K + 4 * u, db[i]);
     }
   }
   __syncthreads();
@@ -759,7 +832,7 @@ relu2_requant_q8_kernel(const int32_t* __restrict__ acc, int64_t H,
   const int4* a4 = reinterpret_cast<const int4*>(acc + m * H);
   const float sc = __fdiv_rn(__fmul_rn(gammaX[m], *g_up), 127.0f);
   auto load_p = [&](int64_t u, float (&v)[8]) {
-    const int4 a = __ldg(a4 + 2 * u), b = __ldg(a4 + 2 * u + 1);
+    const int4 a = __ldg(a4 + unit_column(u) / 4), b = __ldg(a4 + unit_column(u) / 4 + 8);
     const int e[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = fmaxf(__fmul_rn((float)e[j], sc), 0.0f);
@@ -774,7 +847,7 @@ relu2_requant_q8_kernel(const int32_t* __restrict__ acc, int64_t H,
     uint32_t w0, w1;
     const float s = ckpt_codes8<false>(v, w0, w1);
     if (u < units) {
-      *reinterpret_cast<uint2*>(Pq + m * H + 8 * u) = make_uint2(w0, w1);
+      store_unit_bytes(Pq + m * H, unit_column(u), w0, w1);
       if ((u & 7) == 0) ps[(m * H + 8 * u) / 64] = s;
     }
 #pragma unroll
@@ -791,7 +864,7 @@ relu2_requant_q8_kernel(const int32_t* __restrict__ acc, int64_t H,
     const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
     const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
     sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
-    *reinterpret_cast<uint2*>(Rq + m * H + 8 * u) = make_uint2(w0, w1);
+    store_unit_bytes(Rq + m * H, unit_column(u), w0, w1);
   }
   sum = warp_sum_i(sum);
   if ((threadIdx.x & 31) == 0) redi[threadIdx.x >> 5] = sum;
@@ -813,14 +886,16 @@ relu2_grad_q8_kernel(const TD* __restrict__ dR, const uint8_t* __restrict__ Pq,
                      const float* __restrict__ ps, int64_t units, TO* __restrict__ dH) {
   for (int64_t u = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; u < units;
        u += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t c = unit_column(u);
     float d[8];
-    norm_load8(dR + 8 * u, d);
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(Pq + 8 * u));
+    load_unit(dR, c, d);
+    const uint32_t q[2] = {__ldg(reinterpret_cast<const uint32_t*>(Pq + c)),
+                           __ldg(reinterpret_cast<const uint32_t*>(Pq + c + 32))};
     const float s = 2.0f * __ldg(ps + u / 8);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      d[j] *= s * (float)(((j < 4 ? q.x : q.y) >> (8 * (j & 3))) & 255u);
-    norm_store8(dH + 8 * u, d);
+      d[j] *= s * (float)((q[j >> 2] >> (8 * (j & 3))) & 255u);
+    store_unit(dH, c, d);
   }
 }
 
