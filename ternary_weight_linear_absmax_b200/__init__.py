@@ -15,6 +15,8 @@ ReLUSquared).
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _lib
@@ -491,40 +493,50 @@ def bl_ste_grad_weight(dY, A_q, gamma_A, W, gamma, eps: float = 1e-5, *, stream=
 # activation checkpoints.
 
 
-class _On:
-    """Where a call runs: the device of its tensors (all on one) and a stream
-    of that device. Outputs and workspace are allocated on that stream, so that
-    torch does not hand their memory to another one while the call runs."""
+# The current stream's handle and the current device, without the objects that
+# torch.cuda.current_stream() and current_device() go through (3 us a call).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, stream, **tensors):
-        self.device = None
-        for name, t in tensors.items():
-            if t is None:
-                continue
-            _cuda(t, name)
-            if self.device is None:
-                self.device = t.device
-            elif t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, expected {self.device}")
-        self.stream = stream
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"stream is on {stream.device}, expected {self.device}")
 
-    def __enter__(self):
-        index = self.device.index
-        self._guard = None
-        if self.stream is not None:
-            self._guard = torch.cuda.stream(self.stream)
-        elif index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(index)
-        if self._guard is not None:
-            self._guard.__enter__()
-        return torch.cuda.current_stream(index).cuda_stream
+def _placed(fn):
+    """Runs ``fn`` on the device of its first tensor and on ``stream`` (default:
+    that device's current one). Outputs and workspace are allocated on that
+    stream, so that torch does not hand their memory to another one while the
+    call runs."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else next(iter(kw.values()), None)
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            return fn(*args, **kw)      # refused there
+        if stream is not None:
+            if stream.device != first.device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {first.device}")
+            with torch.cuda.stream(stream):
+                return fn(*args, **kw)
+        if first.get_device() != torch._C._cuda_getDevice():
+            with torch.cuda.device(first.device):
+                return fn(*args, **kw)
+        return fn(*args, **kw)
+    return call
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-        return False
+
+def _on(**tensors) -> int:
+    """Checks that the tensors are contiguous and on one CUDA device; returns
+    the handle of that device's current stream."""
+    dev = -1
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        d = t.get_device()
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{name} is on cuda:{d}, expected cuda:{dev}")
+    return _raw_stream(dev)
 
 
 def _of(t, dtype, shape, what: str) -> None:
@@ -533,7 +545,8 @@ def _of(t, dtype, shape, what: str) -> None:
         return
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    _shape(t, shape, what)
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _w4_shapes(N: int, K: int, group: int):
@@ -562,182 +575,189 @@ def _matrix(t: torch.Tensor, what: str):
     return t.shape
 
 
-def bl_quant_weights_w4(W, group: int = 128, *, zeros: bool = False, stream=None):
+@_placed
+def bl_quant_weights_w4(W, group: int = 128, *, zeros: bool = False):
     """4-bit weights with group scales from W [N, K] fp32/bf16: (W4 uint8
     [ceil(N/16), ceil(K/128), 1024], scales bf16 [.., .., 8, 128/group, 2], zero
     points uint8 of that shape, or None when ``zeros`` is false: symmetric)."""
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
-    with _On(stream, W=W) as st:
-        N, K = _matrix(W, "W")
-        w_shape, s_shape = _w4_shapes(N, K, group)
-        W4 = torch.empty(w_shape, dtype=torch.uint8, device=W.device)
-        scales = torch.empty(s_shape, dtype=torch.bfloat16, device=W.device)
-        zp = torch.empty(s_shape, dtype=torch.uint8, device=W.device) if zeros else None
-        check(load().bl_quant_weights_w4(W.data_ptr(), _dt(W, "W"), N, K, group, W4.data_ptr(),
-                                         scales.data_ptr(), _ptr(zp), st), "bl_quant_weights_w4")
+    st = _on(W=W)
+    N, K = _matrix(W, "W")
+    w_shape, s_shape = _w4_shapes(N, K, group)
+    W4 = W.new_empty(w_shape, dtype=torch.uint8)
+    scales = W.new_empty(s_shape, dtype=torch.bfloat16)
+    zp = W.new_empty(s_shape, dtype=torch.uint8) if zeros else None
+    check(load().bl_quant_weights_w4(W.data_ptr(), _dt(W, "W"), N, K, group, W4.data_ptr(),
+                                     scales.data_ptr(), _ptr(zp), st), "bl_quant_weights_w4")
     return W4, scales, zp
 
 
-def bl_pack_w4(codes, scales, group: int = 128, *, zeros=None, stream=None):
+@_placed
+def bl_pack_w4(codes, scales, group: int = 128, *, zeros=None):
     """4-bit weights found elsewhere: codes uint8 [N, K/2] (the lower column in
     the low half of a byte), scales bf16 [N, ceil(K/group)], zero points uint8
     of that shape or None → (W4, scales, zero points) as bl_quant_weights_w4."""
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
-    with _On(stream, codes=codes, scales=scales, zeros=zeros) as st:
-        N, K = _matrix(codes, "codes")
-        K *= 2
-        _of(codes, torch.uint8, (N, K // 2), "codes")
-        _of(scales, torch.bfloat16, (N, -(-K // group)), "scales")
-        _of(zeros, torch.uint8, (N, -(-K // group)), "zeros")
-        w_shape, s_shape = _w4_shapes(N, K, group)
-        W4 = torch.empty(w_shape, dtype=torch.uint8, device=codes.device)
-        out = torch.empty(s_shape, dtype=torch.bfloat16, device=codes.device)
-        zp = None if zeros is None else torch.empty(s_shape, dtype=torch.uint8, device=codes.device)
-        check(load().bl_pack_w4(codes.data_ptr(), scales.data_ptr(), _ptr(zeros), N, K, group,
-                                W4.data_ptr(), out.data_ptr(), _ptr(zp), st), "bl_pack_w4")
+    st = _on(codes=codes, scales=scales, zeros=zeros)
+    N, K = _matrix(codes, "codes")
+    K *= 2
+    _of(codes, torch.uint8, (N, K // 2), "codes")
+    _of(scales, torch.bfloat16, (N, -(-K // group)), "scales")
+    _of(zeros, torch.uint8, (N, -(-K // group)), "zeros")
+    w_shape, s_shape = _w4_shapes(N, K, group)
+    W4 = codes.new_empty(w_shape, dtype=torch.uint8)
+    out = codes.new_empty(s_shape, dtype=torch.bfloat16)
+    zp = None if zeros is None else codes.new_empty(s_shape, dtype=torch.uint8)
+    check(load().bl_pack_w4(codes.data_ptr(), scales.data_ptr(), _ptr(zeros), N, K, group,
+                            W4.data_ptr(), out.data_ptr(), _ptr(zp), st), "bl_pack_w4")
     return W4, out, zp
 
 
-def bl_unpack_w4(W4, scales, N: int, K: int, *, zeros=None, out_dtype=torch.float32, stream=None):
+@_placed
+def bl_unpack_w4(W4, scales, N: int, K: int, *, zeros=None, out_dtype=torch.float32):
     """The matrix [N, K] that packed 4-bit weights stand for."""
-    with _On(stream, W4=W4, scales=scales, zeros=zeros) as st:
-        group = _check_w4(W4, scales, zeros, N, K)
-        out = torch.empty((N, K), dtype=out_dtype, device=W4.device)
-        check(load().bl_unpack_w4(W4.data_ptr(), scales.data_ptr(), _ptr(zeros), N, K, group,
-                                  out.data_ptr(), _dt(out, "out"), st), "bl_unpack_w4")
+    st = _on(W4=W4, scales=scales, zeros=zeros)
+    group = _check_w4(W4, scales, zeros, N, K)
+    out = W4.new_empty((N, K), dtype=out_dtype)
+    check(load().bl_unpack_w4(W4.data_ptr(), scales.data_ptr(), _ptr(zeros), N, K, group,
+                              out.data_ptr(), _dt(out, "out"), st), "bl_unpack_w4")
     return out
 
 
+@_placed
 def bl_linear_w4(X, W4, scales, N: int, *, zeros=None, out_dtype=torch.bfloat16, out=None,
-                 pdl=False, stream=None):
+                 pdl=False):
     """Y [M, N] = X·Wᵀ for few tokens on 4-bit weights with group scales."""
-    with _On(stream, X=X, W4=W4, scales=scales, zeros=zeros, out=out) as st:
-        M, K = _matrix(X, "X")
-        group = _check_w4(W4, scales, zeros, N, K)
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=X.device)
-        _shape(out, (M, N), "out")
-        check(load().bl_linear_w4(X.data_ptr(), _dt(X, "X"), M, K, W4.data_ptr(), scales.data_ptr(),
-                                  _ptr(zeros), N, group, out.data_ptr(), _dt(out, "out"),
-                                  BL_FLAG_PDL if pdl else 0, st), "bl_linear_w4")
+    st = _on(X=X, W4=W4, scales=scales, zeros=zeros, out=out)
+    M, K = _matrix(X, "X")
+    group = _check_w4(W4, scales, zeros, N, K)
+    if out is None:
+        out = X.new_empty((M, N), dtype=out_dtype)
+    _shape(out, (M, N), "out")
+    check(load().bl_linear_w4(X.data_ptr(), _dt(X, "X"), M, K, W4.data_ptr(), scales.data_ptr(),
+                              _ptr(zeros), N, group, out.data_ptr(), _dt(out, "out"),
+                              BL_FLAG_PDL if pdl else 0, st), "bl_linear_w4")
     return out
 
 
-def bl_layernorm(X, weight, bias=None, eps: float = 1e-5, *, out_dtype=torch.bfloat16, stream=None):
+@_placed
+def bl_layernorm(X, weight, bias=None, eps: float = 1e-5, *, out_dtype=torch.bfloat16):
     """Layer norm of the rows of X [M, K]: (Y [M, K], mean fp32 [M], rstd fp32 [M])."""
-    with _On(stream, X=X, weight=weight, bias=bias) as st:
-        M, K = _matrix(X, "X")
-        _of(weight, torch.float32, (K,), "weight")
-        _of(bias, torch.float32, (K,), "bias")
-        Y = torch.empty((M, K), dtype=out_dtype, device=X.device)
-        mean = torch.empty((M,), dtype=torch.float32, device=X.device)
-        rstd = torch.empty((M,), dtype=torch.float32, device=X.device)
-        check(load().bl_layernorm(X.data_ptr(), _dt(X, "X"), M, K, weight.data_ptr(), _ptr(bias),
-                                  float(eps), Y.data_ptr(), _dt(Y, "out"), mean.data_ptr(),
-                                  rstd.data_ptr(), st), "bl_layernorm")
+    st = _on(X=X, weight=weight, bias=bias)
+    M, K = _matrix(X, "X")
+    _of(weight, torch.float32, (K,), "weight")
+    _of(bias, torch.float32, (K,), "bias")
+    Y = X.new_empty((M, K), dtype=out_dtype)
+    mean = X.new_empty((M,), dtype=torch.float32)
+    rstd = X.new_empty((M,), dtype=torch.float32)
+    check(load().bl_layernorm(X.data_ptr(), _dt(X, "X"), M, K, weight.data_ptr(), _ptr(bias),
+                              float(eps), Y.data_ptr(), _dt(Y, "out"), mean.data_ptr(),
+                              rstd.data_ptr(), st), "bl_layernorm")
     return Y, mean, rstd
 
 
+@_placed
 def bl_layernorm_quant(X, weight, bias=None, eps: float = 1e-5, q_eps: float = 1e-5, *,
-                       checkpoint: bool = False, stream=None):
+                       checkpoint: bool = False):
     """Layer norm straight to the int8 tokens that bl_quant_acts would make of
     it: (A_q int8 [M, K], γ_A fp32 [M], Σ A_q int32 [M], rstd fp32 [M], and the
     8-bit checkpoint of the normalised rows for bl_layernorm_grad_q8: int8
     [M, K] and fp32 [M, K/64], or None twice without ``checkpoint``)."""
-    with _On(stream, X=X, weight=weight, bias=bias) as st:
-        M, K = _matrix(X, "X")
-        _of(weight, torch.float32, (K,), "weight")
-        _of(bias, torch.float32, (K,), "bias")
-        dev = X.device
-        A_q = torch.empty((M, K), dtype=torch.int8, device=dev)
-        gamma = torch.empty((M,), dtype=torch.float32, device=dev)
-        rowsum = torch.empty((M,), dtype=torch.int32, device=dev)
-        rstd = torch.empty((M,), dtype=torch.float32, device=dev)
-        xq = torch.empty((M, K), dtype=torch.int8, device=dev) if checkpoint else None
-        xs = torch.empty((M, K // 64), dtype=torch.float32, device=dev) if checkpoint else None
-        check(load().bl_layernorm_quant(X.data_ptr(), _dt(X, "X"), M, K, weight.data_ptr(), _ptr(bias),
-                                        float(eps), float(q_eps), A_q.data_ptr(), gamma.data_ptr(),
-                                        rowsum.data_ptr(), rstd.data_ptr(), _ptr(xq), _ptr(xs), st),
-              "bl_layernorm_quant")
+    st = _on(X=X, weight=weight, bias=bias)
+    M, K = _matrix(X, "X")
+    _of(weight, torch.float32, (K,), "weight")
+    _of(bias, torch.float32, (K,), "bias")
+    A_q = X.new_empty((M, K), dtype=torch.int8)
+    gamma = X.new_empty((M,), dtype=torch.float32)
+    rowsum = X.new_empty((M,), dtype=torch.int32)
+    rstd = X.new_empty((M,), dtype=torch.float32)
+    xq = X.new_empty((M, K), dtype=torch.int8) if checkpoint else None
+    xs = X.new_empty((M, K // 64), dtype=torch.float32) if checkpoint else None
+    check(load().bl_layernorm_quant(X.data_ptr(), _dt(X, "X"), M, K, weight.data_ptr(), _ptr(bias),
+                                    float(eps), float(q_eps), A_q.data_ptr(), gamma.data_ptr(),
+                                    rowsum.data_ptr(), rstd.data_ptr(), _ptr(xq), _ptr(xs), st),
+          "bl_layernorm_quant")
     return A_q, gamma, rowsum, rstd, xq, xs
 
 
-def _norm_grad_out(L, M, K, device, out_dtype):
-    dX = torch.empty((M, K), dtype=out_dtype, device=device)
-    dw = torch.empty((K,), dtype=torch.float32, device=device)
-    db = torch.empty((K,), dtype=torch.float32, device=device)
-    return dX, dw, db, _ws(int(L.bl_layernorm_grad_workspace_bytes(M, K)), device)
+def _norm_grad_out(L, M, K, dY, out_dtype):
+    dX = dY.new_empty((M, K), dtype=out_dtype)
+    dw = dY.new_empty((K,), dtype=torch.float32)
+    db = dY.new_empty((K,), dtype=torch.float32)
+    return dX, dw, db, _ws(int(L.bl_layernorm_grad_workspace_bytes(M, K)), dY.device)
 
 
-def bl_layernorm_grad(dY, X, mean, rstd, weight, *, out_dtype=torch.bfloat16, stream=None):
+@_placed
+def bl_layernorm_grad(dY, X, mean, rstd, weight, *, out_dtype=torch.bfloat16):
     """Layer norm's backward from the kept input: (dX [M, K], dweight fp32 [K], dbias fp32 [K])."""
-    with _On(stream, dY=dY, X=X, mean=mean, rstd=rstd, weight=weight) as st:
-        M, K = _matrix(dY, "dY")
-        _shape(X, (M, K), "X")
-        _of(mean, torch.float32, (M,), "mean")
-        _of(rstd, torch.float32, (M,), "rstd")
-        _of(weight, torch.float32, (K,), "weight")
-        L = load()
-        dX, dw, db, ws = _norm_grad_out(L, M, K, dY.device, out_dtype)
-        check(L.bl_layernorm_grad(dY.data_ptr(), _dt(dY, "dY"), X.data_ptr(), _dt(X, "X"),
-                                  mean.data_ptr(), rstd.data_ptr(), weight.data_ptr(), M, K,
-                                  dX.data_ptr(), _dt(dX, "out"), dw.data_ptr(), db.data_ptr(),
-                                  _ptr(ws), _nbytes(ws), st), "bl_layernorm_grad")
+    st = _on(dY=dY, X=X, mean=mean, rstd=rstd, weight=weight)
+    M, K = _matrix(dY, "dY")
+    _shape(X, (M, K), "X")
+    _of(mean, torch.float32, (M,), "mean")
+    _of(rstd, torch.float32, (M,), "rstd")
+    _of(weight, torch.float32, (K,), "weight")
+    L = load()
+    dX, dw, db, ws = _norm_grad_out(L, M, K, dY, out_dtype)
+    check(L.bl_layernorm_grad(dY.data_ptr(), _dt(dY, "dY"), X.data_ptr(), _dt(X, "X"),
+                              mean.data_ptr(), rstd.data_ptr(), weight.data_ptr(), M, K,
+                              dX.data_ptr(), _dt(dX, "out"), dw.data_ptr(), db.data_ptr(),
+                              _ptr(ws), _nbytes(ws), st), "bl_layernorm_grad")
     return dX, dw, db
 
 
-def bl_layernorm_grad_q8(dY, xhat_q, xhat_scale, rstd, weight, *, out_dtype=torch.bfloat16,
-                         stream=None):
+@_placed
+def bl_layernorm_grad_q8(dY, xhat_q, xhat_scale, rstd, weight, *, out_dtype=torch.bfloat16):
     """Layer norm's backward from the 8-bit checkpoint of the normalised rows:
     (dX [M, K], dweight fp32 [K], dbias fp32 [K])."""
-    with _On(stream, dY=dY, xhat_q=xhat_q, xhat_scale=xhat_scale, rstd=rstd, weight=weight) as st:
-        M, K = _matrix(dY, "dY")
-        _of(xhat_q, torch.int8, (M, K), "xhat_q")
-        _of(xhat_scale, torch.float32, (M, K // 64), "xhat_scale")
-        _of(rstd, torch.float32, (M,), "rstd")
-        _of(weight, torch.float32, (K,), "weight")
-        L = load()
-        dX, dw, db, ws = _norm_grad_out(L, M, K, dY.device, out_dtype)
-        check(L.bl_layernorm_grad_q8(dY.data_ptr(), _dt(dY, "dY"), xhat_q.data_ptr(),
-                                     xhat_scale.data_ptr(), rstd.data_ptr(), weight.data_ptr(), M, K,
-                                     dX.data_ptr(), _dt(dX, "out"), dw.data_ptr(), db.data_ptr(),
-                                     _ptr(ws), _nbytes(ws), st), "bl_layernorm_grad_q8")
+    st = _on(dY=dY, xhat_q=xhat_q, xhat_scale=xhat_scale, rstd=rstd, weight=weight)
+    M, K = _matrix(dY, "dY")
+    _of(xhat_q, torch.int8, (M, K), "xhat_q")
+    _of(xhat_scale, torch.float32, (M, K // 64), "xhat_scale")
+    _of(rstd, torch.float32, (M,), "rstd")
+    _of(weight, torch.float32, (K,), "weight")
+    L = load()
+    dX, dw, db, ws = _norm_grad_out(L, M, K, dY, out_dtype)
+    check(L.bl_layernorm_grad_q8(dY.data_ptr(), _dt(dY, "dY"), xhat_q.data_ptr(),
+                                 xhat_scale.data_ptr(), rstd.data_ptr(), weight.data_ptr(), M, K,
+                                 dX.data_ptr(), _dt(dX, "out"), dw.data_ptr(), db.data_ptr(),
+                                 _ptr(ws), _nbytes(ws), st), "bl_layernorm_grad_q8")
     return dX, dw, db
 
 
-def bl_relu2_requant_q8(acc_up, gamma_x, gamma_up, eps: float = 1e-5, *, stream=None):
+@_placed
+def bl_relu2_requant_q8(acc_up, gamma_x, gamma_up, eps: float = 1e-5):
     """ReLU² of the FFN in training, from the up-projection's INT32 accumulators:
     (R_q int8 [M, H], γ_r fp32 [M], Σ R_q int32 [M], and the 8-bit checkpoint of
     max(h, 0): uint8 [M, H], fp32 [M, H/64])."""
-    with _On(stream, acc_up=acc_up, gamma_x=gamma_x, gamma_up=gamma_up) as st:
-        M, H = _matrix(acc_up, "acc_up")
-        _of(acc_up, torch.int32, (M, H), "acc_up")
-        _of(gamma_x, torch.float32, (M,), "gamma_x")
-        _of(gamma_up, torch.float32, (1,), "gamma_up")
-        dev = acc_up.device
-        R_q = torch.empty((M, H), dtype=torch.int8, device=dev)
-        gamma_r = torch.empty((M,), dtype=torch.float32, device=dev)
-        rowsum = torch.empty((M,), dtype=torch.int32, device=dev)
-        P_q = torch.empty((M, H), dtype=torch.uint8, device=dev)
-        p_scale = torch.empty((M, H // 64), dtype=torch.float32, device=dev)
-        check(load().bl_relu2_requant_q8(acc_up.data_ptr(), gamma_x.data_ptr(), gamma_up.data_ptr(),
-                                         M, H, float(eps), R_q.data_ptr(), gamma_r.data_ptr(),
-                                         rowsum.data_ptr(), P_q.data_ptr(), p_scale.data_ptr(), st),
-              "bl_relu2_requant_q8")
+    st = _on(acc_up=acc_up, gamma_x=gamma_x, gamma_up=gamma_up)
+    M, H = _matrix(acc_up, "acc_up")
+    _of(acc_up, torch.int32, (M, H), "acc_up")
+    _of(gamma_x, torch.float32, (M,), "gamma_x")
+    _of(gamma_up, torch.float32, (1,), "gamma_up")
+    R_q = acc_up.new_empty((M, H), dtype=torch.int8)
+    gamma_r = acc_up.new_empty((M,), dtype=torch.float32)
+    rowsum = acc_up.new_empty((M,), dtype=torch.int32)
+    P_q = acc_up.new_empty((M, H), dtype=torch.uint8)
+    p_scale = acc_up.new_empty((M, H // 64), dtype=torch.float32)
+    check(load().bl_relu2_requant_q8(acc_up.data_ptr(), gamma_x.data_ptr(), gamma_up.data_ptr(),
+                                     M, H, float(eps), R_q.data_ptr(), gamma_r.data_ptr(),
+                                     rowsum.data_ptr(), P_q.data_ptr(), p_scale.data_ptr(), st),
+          "bl_relu2_requant_q8")
     return R_q, gamma_r, rowsum, P_q, p_scale
 
 
-def bl_relu2_grad_q8(dR, P_q, p_scale, *, out_dtype=torch.bfloat16, stream=None):
+@_placed
+def bl_relu2_grad_q8(dR, P_q, p_scale, *, out_dtype=torch.bfloat16):
     """dH [M, H] = 2·p̂·dR from the 8-bit checkpoint of max(h, 0)."""
-    with _On(stream, dR=dR, P_q=P_q, p_scale=p_scale) as st:
-        M, H = _matrix(dR, "dR")
-        _of(P_q, torch.uint8, (M, H), "P_q")
-        _of(p_scale, torch.float32, (M, H // 64), "p_scale")
-        dH = torch.empty((M, H), dtype=out_dtype, device=dR.device)
-        check(load().bl_relu2_grad_q8(dR.data_ptr(), _dt(dR, "dR"), P_q.data_ptr(), p_scale.data_ptr(),
-                                      M, H, dH.data_ptr(), _dt(dH, "out"), st), "bl_relu2_grad_q8")
+    st = _on(dR=dR, P_q=P_q, p_scale=p_scale)
+    M, H = _matrix(dR, "dR")
+    _of(P_q, torch.uint8, (M, H), "P_q")
+    _of(p_scale, torch.float32, (M, H // 64), "p_scale")
+    dH = dR.new_empty((M, H), dtype=out_dtype)
+    check(load().bl_relu2_grad_q8(dR.data_ptr(), _dt(dR, "dR"), P_q.data_ptr(), p_scale.data_ptr(),
+                                  M, H, dH.data_ptr(), _dt(dH, "out"), st), "bl_relu2_grad_q8")
     return dH
 
 

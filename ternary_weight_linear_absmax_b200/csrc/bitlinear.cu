@@ -949,9 +949,6 @@ bl_status launch_w4(const W4Params& p, int group, bool pdl, int dev, int sms, cu
 
 // --------------------------------------------------------------------------
 // Layer norm and 8-bit checkpoints.
-#ifndef NORMTHREADS
-#define NORMTHREADS 640
-#endif
 // Units of eight columns per thread and threads per row: four with many rows
 // (what the threads of a row exchange costs more than their columns do), as
 // few as 512 threads allow with few.
@@ -973,7 +970,9 @@ NormShape norm_shape(int64_t M, int64_t K, int sms) {
 template <typename T, typename OUT, int NU>
 bl_status launch_norm_nu(const NormParams& p, int group, int sms, cudaStream_t st) {
   const int groups = group >= 128 ? 1 : 128 / group;  // at least 128 threads to a CTA
-  const int threads = groups * group, per_sm = NORMTHREADS / threads < 1 ? 1 : NORMTHREADS / threads;
+  // As many CTAs as an SM holds at 128 (64 with fewer units) registers a thread.
+  const int threads = groups * group, room = NU == 4 ? 512 : 1024;
+  const int per_sm = room / threads < 1 ? 1 : room / threads;
   int64_t grid = (p.M + groups - 1) / groups;
   if (grid > (int64_t)per_sm * sms) grid = (int64_t)per_sm * sms;
   if (p.K / 8 == (int64_t)group * NU)
