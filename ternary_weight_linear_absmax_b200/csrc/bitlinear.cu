@@ -851,6 +851,14 @@ bl_status check_group(int group) {
 inline size_t w4_blocks(int64_t N, int64_t K) {
   return (size_t)((N + 15) / 16) * (size_t)((K + 127) / 128);
 }
+// One CTA per row block, and as many along K as give every SM sixteen.
+inline dim3 w4_rows_grid(int64_t N, int64_t K, int sms) {
+  const int64_t RB = (N + 15) / 16, KB = (K + 127) / 128;
+  int64_t y = (16 * (int64_t)sms + RB - 1) / RB;
+  if (y > (KB + 1) / 2) y = (KB + 1) / 2;
+  if (y > 65535) y = 65535;
+  return dim3((unsigned)RB, (unsigned)(y < 1 ? 1 : y));
+}
 // Grid of a loop over `items` work items, `per` to a CTA.
 inline unsigned loop_grid(int64_t items, int64_t per, int sms) {
   int64_t b = (items + per - 1) / per;
@@ -1983,7 +1991,7 @@ bl_status bl_quant_weights_w4(const void* W, bl_dtype w_dtype, int64_t N, int64_
   int dev, sms;
   BL_TRY(current_device(&dev, &sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = loop_grid((int64_t)w4_blocks(N, K) * 16, 16, sms);
+  const dim3 grid = w4_rows_grid(N, K, sms);
   uint32_t* out = reinterpret_cast<uint32_t*>(W4);
   __nv_bfloat16* sc = reinterpret_cast<__nv_bfloat16*>(scales);
   if (w_dtype == BL_BF16)
@@ -2036,10 +2044,9 @@ bl_status bl_unpack_w4(const uint8_t* W4, const void* scales, const uint8_t* zer
   BL_TRY(check_ptr(W));
   int dev, sms;
   BL_TRY(current_device(&dev, &sms));
-  w4_unpack_kernel<<<loop_grid((int64_t)w4_blocks(N, K) * 256, 256, sms), 256, 0,
-                     reinterpret_cast<cudaStream_t>(stream)>>>(
+  w4_unpack_kernel<<<w4_rows_grid(N, K, sms), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       reinterpret_cast<const uint32_t*>(W4), reinterpret_cast<const __nv_bfloat16*>(scales), zeros,
-      N, K, group, W, w_dtype == BL_BF16);
+      N, K, group, W, w_dtype == BL_BF16, (reinterpret_cast<uintptr_t>(W) & 31u) == 0);
   BL_CUDA(cudaGetLastError());
   return BL_OK;
 }

@@ -539,26 +539,25 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 // Round(w ÷ s) to the nearest integer, ties to even, as for the exact
 // quotient, |w| < 16·s. The product with a rounded 1/s is near enough to be off
-// by one at most; the residual w − k·s is exact in fp32 (k·s has 5 + 8 bits), so
-// it says against s/2 whether k is the nearest. s below 2^-60 comes scaled.
+// by one at most; the residual r = w − k·s is exact in fp32 (k·s has 5 + 8
+// bits), so 2·|r| − s says whether k is the nearest: positive, it is off by
+// one, zero, it is one side of a tie. Read as an integer plus the parity of k
+// (the low bit of the sum with 1.5·2^23) it is positive exactly when k has to
+// move towards r. s below 2^-60 comes scaled.
 struct W4Rounder {
-  float s, half, inv, up;
+  float s, inv, up;
   __device__ __forceinline__ explicit W4Rounder(float scale) {
     up = scale < 0x1p-60f ? 0x1p80f : 1.0f;  // exact, and 1/s stays finite
     s = scale * up;
-    half = 0.5f * s;
     inv = s > 0.f ? __fdividef(1.0f, s) : 0.f;
   }
   __device__ __forceinline__ float operator()(float w) const {
     w *= up;
-    float k = __fadd_rn(__fmul_rn(w, inv), 12582912.0f) - 12582912.0f;
-    const float r = fmaf(-k, s, w);
-    if (fabsf(r) >= half) {  // off by one, or a tie
-      const float dir = copysignf(1.0f, r);
-      const bool odd = ((int)k & 1) != 0;
-      if (fabsf(r) > half || (odd && s > 0.f)) k += dir;
-    }
-    return k;
+    const float b = __fadd_rn(__fmul_rn(w, inv), 12582912.0f);
+    const float k = b - 12582912.0f, r = fmaf(-k, s, w);
+    const int c = __float_as_int(fmaf(2.0f, fabsf(r), -s)) + (int)(__float_as_uint(b) & 1u);
+    const float moved = k + copysignf(1.0f, r);
+    return c > 0 ? moved : k;
   }
 };
 
@@ -577,12 +576,17 @@ __device__ __forceinline__ void w4_load8(const T* p, float (&v)[8]) {
   }
 }
 
-// Word of eight codes in column order.
-__device__ __forceinline__ uint32_t w4_word(const uint32_t (&q)[8]) {
-  uint32_t w = 0;
+// Word of eight codes given as floats 0..15: the bits of 2^23 + q are
+// 0x4B000000 + q, and the shifted constants add up to one that is taken off.
+__device__ __forceinline__ uint32_t w4_word(const float (&q)[8]) {
+  uint32_t w = 0, off = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w |= q[j] << (4 * (j >> 1) + 16 * (j & 1));
-  return w;
+  for (int j = 0; j < 8; ++j) {
+    const int sh = 4 * (j >> 1) + 16 * (j & 1);
+    w += __float_as_uint(q[j] + 8388608.0f) << sh;
+    off += 0x4B000000u << sh;
+  }
+  return w - off;
 }
 
 // Where the eight columns 8·l of row r (0..15) of block (rb, kb) are packed.
@@ -593,49 +597,57 @@ __device__ __forceinline__ int64_t w4_group_index(int64_t blk, int r, int v, int
   return ((blk * 8 + (r & 7)) * V + v) * 2 + (r >> 3);
 }
 
+// One CTA per row block (blockIdx.x): sixteen lanes per row, K blocks
+// blockIdx.y, + gridDim.y, ..., two of them under way at a time.
 template <typename T>
 __global__ void __launch_bounds__(256)
 w4_quant_kernel(const T* __restrict__ W, int64_t N, int64_t K, int G, uint32_t* __restrict__ W4,
                 __nv_bfloat16* __restrict__ scales, uint8_t* __restrict__ zeros) {
-  const int64_t KB = (K + 127) / 128, total = (N + 15) / 16 * KB * 16;  // (row block, kb, row)
-  const int l = threadIdx.x & 15, V = 128 / G, gl = G / 8;
-  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 4);
-  const int64_t rounds = (total + step - 1) / step;
-  for (int64_t i = 0; i < rounds; ++i) {  // every lane takes every round: the shuffles need whole warps
-    const int64_t id = (int64_t)blockIdx.x * (blockDim.x >> 4) + (threadIdx.x >> 4) + i * step;
-    const int r = (int)(id & 15);
-    const int64_t blk = id >> 4, rb = blk / KB, kb = blk - rb * KB;
-    const int64_t n = rb * 16 + r, k = kb * 128 + 8 * l;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (id < total && n < N && k < K) w4_load8(W + n * K + k, v);
-    float hi = 0.f, lo = 0.f;
+  const int KB = (int)((K + 127) / 128), l = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int V = 128 / G, gl = G / 8;
+  const int64_t rb = blockIdx.x, n = rb * 16 + r;
+  const T* row = W + n * K + 8 * l;
+  constexpr int B = 2;
+  for (int kb0 = blockIdx.y; kb0 < KB; kb0 += B * gridDim.y) {
+    float v[B][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      hi = fmaxf(hi, v[j]);
-      lo = fminf(lo, v[j]);
-    }
-    for (int o = 1; o < gl; o <<= 1) {
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    }
-    if (id >= total) continue;
-    const float raw = zeros != nullptr ? __fdiv_rn(__fsub_rn(hi, lo), 15.0f)
-                                       : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
-    const __nv_bfloat16 sb = __float2bfloat16_rn(raw);
-    const float s = __bfloat162float(sb);
-    const W4Rounder round(s);
-    float z = 8.0f;
-    if (zeros != nullptr) z = s > 0.f ? fminf(round(-lo), 15.0f) : 0.0f;
-    uint32_t q[8];
+    for (int b = 0; b < B; ++b) {
+      const int64_t k = (int64_t)(kb0 + b * (int)gridDim.y) * 128;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float c = s > 0.f ? fminf(fmaxf(round(v[j]) + z, 0.0f), 15.0f) : z;
-      q[j] = __float_as_uint(c + 8388608.0f) & 15u;
+      for (int j = 0; j < 8; ++j) v[b][j] = 0.f;
+      if (n < N && k + 8 * l < K) w4_load8(row + k, v[b]);
     }
-    W4[w4_word_index(blk, r, l)] = w4_word(q);
-    if (l % gl == 0) {
-      scales[w4_group_index(blk, r, l / gl, V)] = sb;
-      if (zeros != nullptr) zeros[w4_group_index(blk, r, l / gl, V)] = (uint8_t)z;
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int kb = kb0 + b * (int)gridDim.y;
+      if (kb >= KB) break;  // the same for the CTA
+      const int64_t blk = rb * KB + kb;
+      float hi = 0.f, lo = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        hi = fmaxf(hi, v[b][j]);
+        lo = fminf(lo, v[b][j]);
+      }
+      for (int o = 1; o < gl; o <<= 1) {
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      }
+      const float raw = zeros != nullptr ? __fdiv_rn(__fsub_rn(hi, lo), 15.0f)
+                                         : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
+      const __nv_bfloat16 sb = __float2bfloat16_rn(raw);
+      const float s = __bfloat162float(sb);
+      const W4Rounder round(s);
+      float z = 8.0f;
+      if (zeros != nullptr) z = s > 0.f ? fminf(round(-lo), 15.0f) : 0.0f;
+      float q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        q[j] = s > 0.f ? fminf(fmaxf(round(v[b][j]) + z, 0.0f), 15.0f) : z;
+      W4[w4_word_index(blk, r, l)] = w4_word(q);
+      if (l % gl == 0) {
+        scales[w4_group_index(blk, r, l / gl, V)] = sb;
+        if (zeros != nullptr) zeros[w4_group_index(blk, r, l / gl, V)] = (uint8_t)z;
+      }
     }
   }
 }
@@ -656,9 +668,9 @@ w4_pack_kernel(const uint32_t* __restrict__ codes, const __nv_bfloat16* __restri
     const int64_t n = rb * 16 + r, k = kb * 128 + 8 * l;
     const bool in = n < N && k < K;
     const uint32_t c = in ? __ldg(codes + (n * K + k) / 8) : 0u;
-    uint32_t q[8];
+    float q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = (c >> (4 * j)) & 15u;
+    for (int j = 0; j < 8; ++j) q[j] = (float)((c >> (4 * j)) & 15u);
     W4[w4_word_index(blk, r, l)] = w4_word(q);
     if (l % gl == 0) {
       const int64_t o = w4_group_index(blk, r, l / gl, V), src = n * groups + k / G;
@@ -669,35 +681,58 @@ w4_pack_kernel(const uint32_t* __restrict__ codes, const __nv_bfloat16* __restri
 }
 
 // The matrix the packed weights stand for: fl32(s·(q − z)) (exact: 8 + 5 bits),
-// rounded once more for a bf16 output.
+// rounded once more for a bf16 output. CTAs as in the quantiser. `wide`: W is
+// 32-byte aligned, and eight fp32 values go out in one store (whole sectors).
 __global__ void __launch_bounds__(256)
 w4_unpack_kernel(const uint32_t* __restrict__ W4, const __nv_bfloat16* __restrict__ scales,
                  const uint8_t* __restrict__ zeros, int64_t N, int64_t K, int G, void* W,
-                 int w_bf16) {
-  const int64_t KB = (K + 127) / 128, total = (N + 15) / 16 * KB * 256;
+                 int w_bf16, int wide) {
+  const int KB = (int)((K + 127) / 128), l = threadIdx.x & 15, r = threadIdx.x >> 4;
   const int V = 128 / G, gl = G / 8;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int l = (int)(i & 15), r = (int)((i >> 4) & 15);
-    const int64_t blk = i >> 8, rb = blk / KB, kb = blk - rb * KB;
-    const int64_t n = rb * 16 + r, k = kb * 128 + 8 * l;
-    if (n >= N || k >= K) continue;
-    const uint32_t w = __ldg(W4 + w4_word_index(blk, r, l));
-    const int64_t o = w4_group_index(blk, r, l / gl, V);
-    const float s = __bfloat162float(scales[o]);
-    const int z = zeros != nullptr ? zeros[o] : 8;
-    float v[8];
+  const int64_t rb = blockIdx.x, n = rb * 16 + r;
+  if (n >= N) return;
+  constexpr int B = 2;
+  for (int kb0 = blockIdx.y; kb0 < KB; kb0 += B * gridDim.y) {
+    uint32_t w[B];
+    float s[B], z[B];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[j] = __fmul_rn(s, (float)((int)((w >> (4 * (j >> 1) + 16 * (j & 1))) & 15u) - z));
-    if (w_bf16) {
-      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(W) + n * K + k) =
-          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                     pack_bf16x2(v[6], v[7]));
-    } else {
-      float4* out = reinterpret_cast<float4*>(reinterpret_cast<float*>(W) + n * K + k);
-      out[0] = make_float4(v[0], v[1], v[2], v[3]);
-      out[1] = make_float4(v[4], v[5], v[6], v[7]);
+    for (int b = 0; b < B; ++b) {
+      const int kb = kb0 + b * (int)gridDim.y;
+      w[b] = 0u;
+      s[b] = z[b] = 0.f;
+      if (kb * (int64_t)128 + 8 * l < K) {
+        const int64_t blk = rb * KB + kb, o = w4_group_index(blk, r, l / gl, V);
+        w[b] = __ldg(W4 + w4_word_index(blk, r, l));
+        s[b] = __bfloat162float(scales[o]);
+        z[b] = zeros != nullptr ? (float)__ldg(zeros + o) : 8.0f;
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int64_t k = (int64_t)(kb0 + b * (int)gridDim.y) * 128 + 8 * l;
+      if (k >= K) break;
+      const float base = 8388608.0f + z[b];
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t q = (w[b] >> (4 * (j >> 1) + 16 * (j & 1))) & 15u;
+        v[j] = __fmul_rn(s[b], __uint_as_float(0x4B000000u | q) - base);
+      }
+      if (w_bf16) {
+        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(W) + n * K + k) =
+            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7]));
+      } else {
+        float* out = reinterpret_cast<float*>(W) + n * K + k;
+        if (wide) {
+          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "f"(v[0]),
+                       "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                       : "memory");
+        } else {
+          reinterpret_cast<float4*>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      }
     }
   }
 }
