@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "bitlinear.h"
 #include "bl_device.cuh"
@@ -847,6 +848,15 @@ bl_status run_bf16_gemm(const void* A, int64_t lda, const void* B, int64_t ldb, 
 // 4-bit weights.
 bl_status check_group(int group) {
   return group == 32 || group == 64 || group == 128 ? BL_OK : BL_ERR_SHAPE;
+}
+template <typename F>
+void for_group(int group, F&& f) {
+  if (group == 32)
+    f(std::integral_constant<int, 32>());
+  else if (group == 64)
+    f(std::integral_constant<int, 64>());
+  else
+    f(std::integral_constant<int, 128>());
 }
 inline size_t w4_blocks(int64_t N, int64_t K) {
   return (size_t)((N + 15) / 16) * (size_t)((K + 127) / 128);
@@ -1994,12 +2004,18 @@ bl_status bl_quant_weights_w4(const void* W, bl_dtype w_dtype, int64_t N, int64_
   const dim3 grid = w4_rows_grid(N, K, sms);
   uint32_t* out = reinterpret_cast<uint32_t*>(W4);
   __nv_bfloat16* sc = reinterpret_cast<__nv_bfloat16*>(scales);
+  auto launch = [&](auto* w, auto g) {
+    constexpr int G = decltype(g)::value;
+    using T = std::remove_const_t<std::remove_pointer_t<decltype(w)>>;
+    if (zeros != nullptr)
+      w4_quant_kernel<T, G, true><<<grid, 256, 0, st>>>(w, N, K, out, sc, zeros);
+    else
+      w4_quant_kernel<T, G, false><<<grid, 256, 0, st>>>(w, N, K, out, sc, zeros);
+  };
   if (w_dtype == BL_BF16)
-    w4_quant_kernel<<<grid, 256, 0, st>>>(reinterpret_cast<const __nv_bfloat16*>(W), N, K, group,
-                                          out, sc, zeros);
+    for_group(group, [&](auto g) { launch(reinterpret_cast<const __nv_bfloat16*>(W), g); });
   else
-    w4_quant_kernel<<<grid, 256, 0, st>>>(reinterpret_cast<const float*>(W), N, K, group, out, sc,
-                                          zeros);
+    for_group(group, [&](auto g) { launch(reinterpret_cast<const float*>(W), g); });
   BL_CUDA(cudaGetLastError());
   return BL_OK;
 }
@@ -2044,9 +2060,12 @@ bl_status bl_unpack_w4(const uint8_t* W4, const void* scales, const uint8_t* zer
   BL_TRY(check_ptr(W));
   int dev, sms;
   BL_TRY(current_device(&dev, &sms));
-  w4_unpack_kernel<<<w4_rows_grid(N, K, sms), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      reinterpret_cast<const uint32_t*>(W4), reinterpret_cast<const __nv_bfloat16*>(scales), zeros,
-      N, K, group, W, w_dtype == BL_BF16, (reinterpret_cast<uintptr_t>(W) & 31u) == 0);
+  for_group(group, [&](auto g) {
+    w4_unpack_kernel<decltype(g)::value>
+        <<<w4_rows_grid(N, K, sms), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+            reinterpret_cast<const uint32_t*>(W4), reinterpret_cast<const __nv_bfloat16*>(scales),
+            zeros, N, K, W, w_dtype == BL_BF16, (reinterpret_cast<uintptr_t>(W) & 31u) == 0);
+  });
   BL_CUDA(cudaGetLastError());
   return BL_OK;
 }

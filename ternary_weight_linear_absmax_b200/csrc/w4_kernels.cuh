@@ -547,7 +547,8 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 struct W4Rounder {
   float s, inv, up;
   __device__ __forceinline__ explicit W4Rounder(float scale) {
-    up = scale < 0x1p-60f ? 0x1p80f : 1.0f;  // exact, and 1/s stays finite
+    // exact, and 1/s stays finite; a scale of 0 makes every value 0
+    up = scale > 0.f ? (scale < 0x1p-60f ? 0x1p80f : 1.0f) : 0.f;
     s = scale * up;
     inv = s > 0.f ? __fdividef(1.0f, s) : 0.f;
   }
@@ -599,12 +600,12 @@ __device__ __forceinline__ int64_t w4_group_index(int64_t blk, int r, int v, int
 
 // One CTA per row block (blockIdx.x): sixteen lanes per row, K blocks
 // blockIdx.y, + gridDim.y, ..., two of them under way at a time.
-template <typename T>
+template <typename T, int G, bool ZP>
 __global__ void __launch_bounds__(256)
-w4_quant_kernel(const T* __restrict__ W, int64_t N, int64_t K, int G, uint32_t* __restrict__ W4,
+w4_quant_kernel(const T* __restrict__ W, int64_t N, int64_t K, uint32_t* __restrict__ W4,
                 __nv_bfloat16* __restrict__ scales, uint8_t* __restrict__ zeros) {
   const int KB = (int)((K + 127) / 128), l = threadIdx.x & 15, r = threadIdx.x >> 4;
-  const int V = 128 / G, gl = G / 8;
+  constexpr int V = 128 / G, gl = G / 8;
   const int64_t rb = blockIdx.x, n = rb * 16 + r;
   const T* row = W + n * K + 8 * l;
   constexpr int B = 2;
@@ -622,31 +623,28 @@ w4_quant_kernel(const T* __restrict__ W, int64_t N, int64_t K, int G, uint32_t* 
       const int kb = kb0 + b * (int)gridDim.y;
       if (kb >= KB) break;  // the same for the CTA
       const int64_t blk = rb * KB + kb;
-      float hi = 0.f, lo = 0.f;
+      float hi = 0.f, lo = 0.f;  // without zero points: hi of the magnitudes
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        hi = fmaxf(hi, v[b][j]);
-        lo = fminf(lo, v[b][j]);
+        hi = fmaxf(hi, ZP ? v[b][j] : fabsf(v[b][j]));
+        if (ZP) lo = fminf(lo, v[b][j]);
       }
+#pragma unroll
       for (int o = 1; o < gl; o <<= 1) {
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        if (ZP) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       }
-      const float raw = zeros != nullptr ? __fdiv_rn(__fsub_rn(hi, lo), 15.0f)
-                                         : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
+      const float raw = ZP ? __fdiv_rn(__fsub_rn(hi, lo), 15.0f) : __fdiv_rn(hi, 7.0f);
       const __nv_bfloat16 sb = __float2bfloat16_rn(raw);
-      const float s = __bfloat162float(sb);
-      const W4Rounder round(s);
-      float z = 8.0f;
-      if (zeros != nullptr) z = s > 0.f ? fminf(round(-lo), 15.0f) : 0.0f;
+      const W4Rounder round(__bfloat162float(sb));
+      const float z = ZP ? fminf(round(-lo), 15.0f) : 8.0f;
       float q[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        q[j] = s > 0.f ? fminf(fmaxf(round(v[b][j]) + z, 0.0f), 15.0f) : z;
+      for (int j = 0; j < 8; ++j) q[j] = fminf(fmaxf(round(v[b][j]) + z, 0.0f), 15.0f);
       W4[w4_word_index(blk, r, l)] = w4_word(q);
       if (l % gl == 0) {
         scales[w4_group_index(blk, r, l / gl, V)] = sb;
-        if (zeros != nullptr) zeros[w4_group_index(blk, r, l / gl, V)] = (uint8_t)z;
+        if (ZP) zeros[w4_group_index(blk, r, l / gl, V)] = (uint8_t)z;
       }
     }
   }
@@ -683,15 +681,16 @@ w4_pack_kernel(const uint32_t* __restrict__ codes, const __nv_bfloat16* __restri
 // The matrix the packed weights stand for: fl32(s·(q − z)) (exact: 8 + 5 bits),
 // rounded once more for a bf16 output. CTAs as in the quantiser. `wide`: W is
 // 32-byte aligned, and eight fp32 values go out in one store (whole sectors).
+template <int G>
 __global__ void __launch_bounds__(256)
 w4_unpack_kernel(const uint32_t* __restrict__ W4, const __nv_bfloat16* __restrict__ scales,
-                 const uint8_t* __restrict__ zeros, int64_t N, int64_t K, int G, void* W,
-                 int w_bf16, int wide) {
+                 const uint8_t* __restrict__ zeros, int64_t N, int64_t K, void* W, int w_bf16,
+                 int wide) {
   const int KB = (int)((K + 127) / 128), l = threadIdx.x & 15, r = threadIdx.x >> 4;
-  const int V = 128 / G, gl = G / 8;
+  constexpr int V = 128 / G, gl = G / 8;
   const int64_t rb = blockIdx.x, n = rb * 16 + r;
   if (n >= N) return;
-  constexpr int B = 2;
+  constexpr int B = 4;
   for (int kb0 = blockIdx.y; kb0 < KB; kb0 += B * gridDim.y) {
     uint32_t w[B];
     float s[B], z[B];
@@ -704,19 +703,19 @@ w4_unpack_kernel(const uint32_t* __restrict__ W4, const __nv_bfloat16* __restric
         const int64_t blk = rb * KB + kb, o = w4_group_index(blk, r, l / gl, V);
         w[b] = __ldg(W4 + w4_word_index(blk, r, l));
         s[b] = __bfloat162float(scales[o]);
-        z[b] = zeros != nullptr ? (float)__ldg(zeros + o) : 8.0f;
+        // 2^23 + z
+        z[b] = __uint_as_float(0x4B000000u | (zeros != nullptr ? __ldg(zeros + o) : 8u));
       }
     }
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       const int64_t k = (int64_t)(kb0 + b * (int)gridDim.y) * 128 + 8 * l;
       if (k >= K) break;
-      const float base = 8388608.0f + z[b];
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t q = (w[b] >> (4 * (j >> 1) + 16 * (j & 1))) & 15u;
-        v[j] = __fmul_rn(s[b], __uint_as_float(0x4B000000u | q) - base);
+        v[j] = __fmul_rn(s[b], __uint_as_float(0x4B000000u | q) - z[b]);
       }
       if (w_bf16) {
         *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(W) + n * K + k) =
