@@ -967,38 +967,58 @@ bl_status launch_w4(const W4Params& p, int group, bool pdl, int dev, int sms, cu
 
 // --------------------------------------------------------------------------
 // Layer norm and 8-bit checkpoints.
-// Units of eight columns per thread and threads per row: four with many rows
-// (what the threads of a row exchange costs more than their columns do), as
-// few as 512 threads allow with few.
+// Units of eight columns per thread and threads per row. With many rows, four
+// while a row then takes at most 256 threads (what the threads of a row
+// exchange costs more than their columns do), else two, for which an SM holds
+// twice the warps, else four again. With few rows, as few units as fit.
 struct NormShape {
   int nu, group;  // nu 0: the row is too long for registers
 };
 NormShape norm_shape(int64_t M, int64_t K, int sms) {
   const int64_t units = K / 8;
-  for (int nu = M >= 2 * sms ? 4 : 1; nu <= 4; nu *= 2) {
-    const int64_t group = ((units + nu - 1) / nu + 31) / 32 * 32;
-    if (group > kNormMaxThreads) continue;
-    int need = 1;  // no more units than such a group needs
-    while (need * group < units) need *= 2;
-    return {need, (int)group};
-  }
-  return {0, 0};
+  auto group = [&](int nu) { return ((units + nu - 1) / nu + 31) / 32 * 32; };
+  int nu = 1;
+  if (M >= 2 * sms)
+    nu = group(4) <= 256 ? 4 : 2;
+  while (nu <= 4 && group(nu) > norm_threads(nu)) nu *= 2;
+  if (nu > 4) return {0, 0};
+  const int64_t g = group(nu);
+  while (nu > 1 && nu / 2 * g >= units) nu /= 2;  // no more units than such a group needs
+  return {nu, (int)g};
+}
+
+// Grid and threads of the row kernels: at least 128 threads to a CTA, and as
+// many CTAs as an SM holds at 128 (64 with fewer than four units) registers a
+// thread.
+struct RowGrid {
+  unsigned grid, threads;
+};
+RowGrid row_grid(int64_t M, int nu, int group, int sms) {
+  const int groups = group >= 128 ? 1 : 128 / group;
+  const int threads = groups * group, room = nu == 4 ? 512 : 1024;
+  const int per_sm = room / threads < 1 ? 1 : room / threads;
+  int64_t grid = (M + groups - 1) / groups;
+  if (grid > (int64_t)per_sm * sms) grid = (int64_t)per_sm * sms;
+  return {(unsigned)grid, (unsigned)threads};
 }
 
 template <typename T, typename OUT, int NU>
 bl_status launch_norm_nu(const NormParams& p, int group, int sms, cudaStream_t st) {
-  const int groups = group >= 128 ? 1 : 128 / group;  // at least 128 threads to a CTA
-  // As many CTAs as an SM holds at 128 (64 with fewer units) registers a thread.
-  const int threads = groups * group, room = NU == 4 ? 512 : 1024;
-  const int per_sm = room / threads < 1 ? 1 : room / threads;
-  int64_t grid = (p.M + groups - 1) / groups;
-  if (grid > (int64_t)per_sm * sms) grid = (int64_t)per_sm * sms;
+  const RowGrid r = row_grid(p.M, NU, group, sms);
   if (p.K / 8 == (int64_t)group * NU)
-    layernorm_kernel<T, OUT, NU, true><<<(unsigned)grid, threads, 0, st>>>(p, group);
+    layernorm_kernel<T, OUT, NU, true><<<r.grid, r.threads, 0, st>>>(p, group);
   else
-    layernorm_kernel<T, OUT, NU, false><<<(unsigned)grid, threads, 0, st>>>(p, group);
+    layernorm_kernel<T, OUT, NU, false><<<r.grid, r.threads, 0, st>>>(p, group);
   BL_CUDA(cudaGetLastError());
   return BL_OK;
+}
+template <int NU>
+void launch_relu2(const Relu2Params& p, int group, int sms, cudaStream_t st) {
+  const RowGrid r = row_grid(p.M, NU, group, sms);
+  if (p.H / 8 == (int64_t)group * NU)
+    relu2_requant_q8_kernel<NU, true><<<r.grid, r.threads, 0, st>>>(p, group);
+  else
+    relu2_requant_q8_kernel<NU, false><<<r.grid, r.threads, 0, st>>>(p, group);
 }
 template <typename T, typename OUT>
 bl_status launch_norm_out(const NormParams& p, int sms, cudaStream_t st) {
@@ -2222,8 +2242,17 @@ bl_status bl_relu2_requant_q8(const int32_t* acc_up, const float* gamma_x, const
   BL_TRY(check_ptr(p_scale));
   int dev, sms;
   BL_TRY(current_device(&dev, &sms));
-  relu2_requant_q8_kernel<<<(unsigned)M, kNormThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      acc_up, H, gamma_x, gamma_up, eps, R_q, gamma_r, rowsum, P_q, p_scale);
+  const Relu2Params p = {acc_up, gamma_x, gamma_up, M, H, eps, R_q, gamma_r, rowsum, P_q, p_scale};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const NormShape s = norm_shape(M, H, sms);
+  if (s.nu == 1)
+    launch_relu2<1>(p, s.group, sms, st);
+  else if (s.nu == 2)
+    launch_relu2<2>(p, s.group, sms, st);
+  else if (s.nu == 4)
+    launch_relu2<4>(p, s.group, sms, st);
+  else
+    relu2_requant_q8_long_kernel<<<(unsigned)M, kNormThreads, 0, st>>>(p);
   BL_CUDA(cudaGetLastError());
   return BL_OK;
 }
@@ -2244,7 +2273,7 @@ bl_status bl_relu2_grad_q8(const void* dR, bl_dtype dr_dtype, const uint8_t* P_q
   BL_TRY(current_device(&dev, &sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t units = M * (H / 8);
-  const unsigned grid = loop_grid(units, kNormThreads, sms);
+  const unsigned grid = loop_grid(units, 4 * kNormThreads, sms);
   const float* df = reinterpret_cast<const float*>(dR);
   const __nv_bfloat16* db = reinterpret_cast<const __nv_bfloat16*>(dR);
   float* of = reinterpret_cast<float*>(dH);

@@ -20,7 +20,8 @@
 namespace bl {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormMaxThreads = 512;
+// Threads of a row kernel's CTA, at 64 (128) registers each.
+__host__ __device__ constexpr int norm_threads(int nu) { return nu <= 2 ? 1024 : 512; }
 constexpr float kCkptTiny = 7.888609052210118e-31f;  // 2^-100
 
 // Eight consecutive elements as fp32.
@@ -165,6 +166,45 @@ __device__ __forceinline__ float ckpt_codes8(const float (&v)[8], uint32_t& w0, 
   return live ? __fdiv_rn(m, top) : 0.f;
 }
 
+// Checkpoint codes of NU units (at most eight) per thread, eight neighbouring
+// lanes to a group of each unit. The divisions of all the units' groups are
+// done at once: lane i of a group takes unit i's maximum. Returns unit i's scale
+// in lane i of its group.
+template <bool SIGNED, int NU>
+__device__ __forceinline__ float ckpt_codes(const float (&v)[NU][8], uint32_t (&w)[NU][2]) {
+  constexpr float top = SIGNED ? 127.0f : 255.0f;
+  const int l = threadIdx.x & 7;
+  float mine = 0.f;
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[i][j]));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (l == i) mine = m;
+  }
+  const bool live = mine >= kCkptTiny;
+  const float inv_mine = live ? __fdiv_rn(top, mine) : 0.f;
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const float inv = __shfl_sync(0xffffffffu, inv_mine, (threadIdx.x & 24) + i);
+    uint32_t b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)  // the sum's low byte is the rounded integer (ties to even)
+      b[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[i][j], inv), 12582912.0f));
+    w[i][0] = pack4_low_bytes(b[0], b[1], b[2], b[3]);
+    w[i][1] = pack4_low_bytes(b[4], b[5], b[6], b[7]);
+  }
+  return live ? __fdiv_rn(mine, top) : 0.f;
+}
+
+// quant_i8_bits for values that the scale keeps within the int8 range: with
+// s = 127/(max + eps), |v·s| < 127.5, so nothing is clipped.
+__device__ __forceinline__ uint32_t token_bits(float v, float s) {
+  return __float_as_uint(__fadd_rn(__fmul_rn(v, s), 12582912.0f));
+}
+
 // ---------------------------------------------------------------------------
 // Forward, one CTA per row, eight columns per thread and step.
 struct NormParams {
@@ -280,7 +320,7 @@ struct RawUnit {
 // FULL: the units are T·NU, every thread has all of its own. OUT: fp32/bf16
 // rows, or int8_t for the tokens.
 template <typename T, typename OUT, int NU, bool FULL>
-__global__ void __launch_bounds__(kNormMaxThreads) layernorm_kernel(const NormParams p, int group) {
+__global__ void __launch_bounds__(norm_threads(NU)) layernorm_kernel(const NormParams p, int group) {
   __shared__ double redd[2][32];
   __shared__ float redf[32];
   __shared__ int redi[32];
@@ -344,23 +384,30 @@ __global__ void __launch_bounds__(kNormMaxThreads) layernorm_kernel(const NormPa
       }
     } else {
       float mx = 0.f;
+      if (p.xq != nullptr) {  // x̂ for the checkpoint first: y takes its place below
 #pragma unroll
-      for (int i = 0; i < NU; ++i) {  // whole warps: a checkpoint group is eight lanes
-        const int u = g.tid + i * g.T;
+        for (int i = 0; i < NU; ++i) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) xhat[j] = 0.f;
+          for (int j = 0; j < 8; ++j) v[i][j] = has(i) ? __fmul_rn(v[i][j], rstd) : 0.f;
+        }
+        uint32_t w[NU][2];
+        const float sc = ckpt_codes<true, NU>(v, w);
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+          const int u = g.tid + i * g.T;
+          if (has(i)) {
+            store_unit_bytes(p.xq + m * p.K, unit_column(u), w[i][0], w[i][1]);
+            if ((u & 7) == i) p.xs[(m * p.K + 8 * u) / 64] = sc;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
         if (has(i)) {
-          norm_affine_unit(v[i], rstd, p.weight, p.bias, unit_column(u), xhat, v[i]);
+          norm_affine_unit(v[i], p.xq != nullptr ? 1.0f : rstd, p.weight, p.bias,
+                           unit_column(g.tid + i * g.T), xhat, v[i]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[i][j]));
-        }
-        if (p.xq != nullptr) {
-          uint32_t w0, w1;
-          const float sc = ckpt_codes8<true>(xhat, w0, w1);
-          if (has(i)) {
-            store_unit_bytes(p.xq + m * p.K, unit_column(u), w0, w1);
-            if ((u & 7) == 0) p.xs[(m * p.K + 8 * u) / 64] = sc;
-          }
         }
       }
       mx = group_reduce(g, mx, redf, [](float a, float b) { return fmaxf(a, b); });
@@ -371,7 +418,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) layernorm_kernel(const NormPa
         if (has(i)) {
           uint32_t b[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) b[j] = quant_i8_bits(v[i][j], scale);
+          for (int j = 0; j < 8; ++j) b[j] = token_bits(v[i][j], scale);
           const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
           const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
           sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
@@ -456,7 +503,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
       norm_affine_unit(x, rstd, p.weight, p.bias, unit_column(u), xhat, y);
       uint32_t b[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) b[j] = quant_i8_bits(y[j], scale);
+      for (int j = 0; j < 8; ++j) b[j] = token_bits(y[j], scale);
       const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
       const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
       sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
@@ -818,19 +865,109 @@ norm_colsum_kernel(const float* __restrict__ part, int parts, int64_t K, float* 
 // ---------------------------------------------------------------------------
 // ReLU² of the FFN's hidden layer in training: from the up-projection's INT32
 // accumulators, the requantised tokens of the down-projection (the arithmetic
-// of relu2_requant_kernel) and an 8-bit checkpoint of p = max(h, 0). One CTA
-// per token.
-__global__ void __launch_bounds__(kNormThreads)
-relu2_requant_q8_kernel(const int32_t* __restrict__ acc, int64_t H,
-                        const float* __restrict__ gammaX, const float* __restrict__ g_up, float eps,
-                        int8_t* __restrict__ Rq, float* __restrict__ gammaR,
-                        int32_t* __restrict__ rowsum, uint8_t* __restrict__ Pq,
-                        float* __restrict__ ps) {
+// of relu2_requant_kernel) and an 8-bit checkpoint of p = max(h, 0). One row
+// per group of T threads at a time, in registers between the checkpoint and
+// the tokens, the next row on its way. FULL as in layernorm_kernel.
+struct Relu2Params {
+  const int32_t* acc;   // [M, H]
+  const float* gammaX;  // [M]
+  const float* g_up;    // 1
+  int64_t M, H;
+  float eps;
+  int8_t* Rq;           // [M, H]
+  float* gammaR;        // [M]
+  int32_t* rowsum;      // [M] or null
+  uint8_t* Pq;          // [M, H]
+  float* ps;            // [M, H/64]
+};
+
+template <int NU, bool FULL>
+__global__ void __launch_bounds__(norm_threads(NU)) relu2_requant_q8_kernel(const Relu2Params p, int group) {
+  __shared__ float redf[32];
+  __shared__ int redi[32];
+  const RowGroup g(group);
+  const int units = (int)(p.H / 8), groups = (int)blockDim.x / group;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  auto has = [&](int i) { return FULL || g.tid + i * g.T < units; };
+  int4 raw[NU][2];
+  float gx = 0.f;
+  auto load = [&](int64_t m) {
+    if (m >= p.M) return;
+    gx = __ldg(p.gammaX + m);
+    const int32_t* row = p.acc + m * p.H;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      if (has(i)) {
+        const int64_t c = unit_column(g.tid + i * g.T);
+        raw[i][0] = __ldg(reinterpret_cast<const int4*>(row + c));
+        raw[i][1] = __ldg(reinterpret_cast<const int4*>(row + c + 32));
+      }
+    }
+  };
+  const float up = __ldg(p.g_up);
+  int64_t m = (int64_t)blockIdx.x * groups + g.id;
+  load(m);
+  for (; m < p.M; m += step) {
+    const float sc = __fdiv_rn(__fmul_rn(gx, up), 127.0f);
+    float v[NU][8], mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+      if (has(i)) {
+        const int e[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
+                          raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = fmaxf(__fmul_rn((float)e[j], sc), 0.0f);
+      }
+    }
+    load(m + step);
+    uint32_t w[NU][2];
+    const float sc8 = ckpt_codes<false, NU>(v, w);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int u = g.tid + i * g.T;
+      if (has(i)) {
+        store_unit_bytes(p.Pq + m * p.H, unit_column(u), w[i][0], w[i][1]);
+        if ((u & 7) == i) p.ps[(m * p.H + 8 * u) / 64] = sc8;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] = __fmul_rn(v[i][j], v[i][j]);
+        mx = fmaxf(mx, v[i][j]);
+      }
+    }
+    mx = group_reduce(g, mx, redf, [](float a, float b) { return fmaxf(a, b); });
+    const float s = __fdiv_rn(127.0f, __fadd_rn(mx, p.eps));
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      if (has(i)) {
+        uint32_t b[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = token_bits(v[i][j], s);
+        const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
+        const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
+        sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
+        store_unit_bytes(p.Rq + m * p.H, unit_column(g.tid + i * g.T), w0, w1);
+      }
+    }
+    // also keeps the maxima from being written for the next row while they are read
+    sum = group_reduce(g, sum, redi, [](int a, int b) { return a + b; });
+    if (g.tid == 0) {
+      p.gammaR[m] = mx;
+      if (p.rowsum != nullptr) p.rowsum[m] = sum;
+    }
+  }
+}
+
+// Rows longer than a CTA's registers hold: the second pass reads them again.
+__global__ void __launch_bounds__(kNormThreads) relu2_requant_q8_long_kernel(const Relu2Params p) {
   __shared__ float redf[kNormThreads / 32];
   __shared__ int redi[kNormThreads / 32];
-  const int64_t m = blockIdx.x, units = H / 8;
-  const int4* a4 = reinterpret_cast<const int4*>(acc + m * H);
-  const float sc = __fdiv_rn(__fmul_rn(gammaX[m], *g_up), 127.0f);
+  const int64_t m = blockIdx.x, units = p.H / 8;
+  const int4* a4 = reinterpret_cast<const int4*>(p.acc + m * p.H);
+  const float sc = __fdiv_rn(__fmul_rn(p.gammaX[m], *p.g_up), 127.0f);
   auto load_p = [&](int64_t u, float (&v)[8]) {
     const int4 a = __ldg(a4 + unit_column(u) / 4), b = __ldg(a4 + unit_column(u) / 4 + 8);
     const int e[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -847,55 +984,73 @@ relu2_requant_q8_kernel(const int32_t* __restrict__ acc, int64_t H,
     uint32_t w0, w1;
     const float s = ckpt_codes8<false>(v, w0, w1);
     if (u < units) {
-      store_unit_bytes(Pq + m * H, unit_column(u), w0, w1);
-      if ((u & 7) == 0) ps[(m * H + 8 * u) / 64] = s;
+      store_unit_bytes(p.Pq + m * p.H, unit_column(u), w0, w1);
+      if ((u & 7) == 0) p.ps[(m * p.H + 8 * u) / 64] = s;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) mx = fmaxf(mx, __fmul_rn(v[j], v[j]));
   }
   mx = block_max_f(mx, redf);
-  const float s = __fdiv_rn(127.0f, __fadd_rn(mx, eps));
+  const float s = __fdiv_rn(127.0f, __fadd_rn(mx, p.eps));
   int sum = 0;
   for (int64_t u = threadIdx.x; u < units; u += kNormThreads) {
     load_p(u, v);
     uint32_t b[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) b[j] = quant_i8_bits(__fmul_rn(v[j], v[j]), s);
+    for (int j = 0; j < 8; ++j) b[j] = token_bits(__fmul_rn(v[j], v[j]), s);
     const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
     const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
     sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
-    store_unit_bytes(Rq + m * H, unit_column(u), w0, w1);
+    store_unit_bytes(p.Rq + m * p.H, unit_column(u), w0, w1);
   }
   sum = warp_sum_i(sum);
   if ((threadIdx.x & 31) == 0) redi[threadIdx.x >> 5] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
-    gammaR[m] = mx;
-    if (rowsum != nullptr) {
+    p.gammaR[m] = mx;
+    if (p.rowsum != nullptr) {
       int t = 0;
       for (int w = 0; w < kNormThreads / 32; ++w) t += redi[w];
-      rowsum[m] = t;
+      p.rowsum[m] = t;
     }
   }
 }
 
-// dH = 2·p̂·dR, p̂ = scale·code: eight columns per thread.
+// dH = 2·p̂·dR, p̂ = scale·code: units of eight columns, four of them under way
+// per thread.
 template <typename TD, typename TO>
 __global__ void __launch_bounds__(kNormThreads)
 relu2_grad_q8_kernel(const TD* __restrict__ dR, const uint8_t* __restrict__ Pq,
                      const float* __restrict__ ps, int64_t units, TO* __restrict__ dH) {
-  for (int64_t u = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; u < units;
-       u += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t c = unit_column(u);
-    float d[8];
-    load_unit(dR, c, d);
-    const uint32_t q[2] = {__ldg(reinterpret_cast<const uint32_t*>(Pq + c)),
-                           __ldg(reinterpret_cast<const uint32_t*>(Pq + c + 32))};
-    const float s = 2.0f * __ldg(ps + u / 8);
+  constexpr int B = 4;
+  const int64_t step = (int64_t)gridDim.x * kNormThreads;
+  for (int64_t u0 = blockIdx.x * (int64_t)kNormThreads + threadIdx.x; u0 < units; u0 += B * step) {
+    RawUnit<TD> raw[B];
+    uint32_t q[B][2];
+    float s[B];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      d[j] *= s * (float)((q[j >> 2] >> (8 * (j & 3))) & 255u);
-    store_unit(dH, c, d);
+    for (int b = 0; b < B; ++b) {
+      const int64_t u = u0 + b * step, c = unit_column(u);
+      if (u < units) {
+        raw[b].load(dR, c);
+        q[b][0] = __ldg(reinterpret_cast<const uint32_t*>(Pq + c));
+        q[b][1] = __ldg(reinterpret_cast<const uint32_t*>(Pq + c + 32));
+        s[b] = __ldg(ps + u / 8);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int64_t u = u0 + b * step;
+      if (u < units) {
+        float d[8];
+        raw[b].get(d);
+        const float s2 = 2.0f * s[b];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)  // the code in the low bits of 2^23
+          d[j] *= s2 * (__uint_as_float(__byte_perm(q[b][j >> 2], 0x4B000000u, 0x7540 | (j & 3))) - 8388608.0f);
+        store_unit(dH, unit_column(u), d);
+      }
+    }
   }
 }
 
