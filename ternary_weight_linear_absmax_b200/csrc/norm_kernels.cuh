@@ -866,8 +866,8 @@ norm_colsum_kernel(const float* __restrict__ part, int parts, int64_t K, float* 
 // ReLU² of the FFN's hidden layer in training: from the up-projection's INT32
 // accumulators, the requantised tokens of the down-projection (the arithmetic
 // of relu2_requant_kernel) and an 8-bit checkpoint of p = max(h, 0). One row
-// per group of T threads at a time, in registers between the checkpoint and
-// the tokens, the next row on its way. FULL as in layernorm_kernel.
+// per group of T threads, in registers between the checkpoint and the tokens.
+// FULL as in layernorm_kernel.
 struct Relu2Params {
   const int32_t* acc;   // [M, H]
   const float* gammaX;  // [M]
@@ -882,86 +882,75 @@ struct Relu2Params {
 };
 
 template <int NU, bool FULL>
-__global__ void __launch_bounds__(norm_threads(NU)) relu2_requant_q8_kernel(const Relu2Params p, int group) {
+__global__ void __launch_bounds__(512, 2) relu2_requant_q8_kernel(const Relu2Params p, int group) {
   __shared__ float redf[32];
   __shared__ int redi[32];
   const RowGroup g(group);
   const int units = (int)(p.H / 8), groups = (int)blockDim.x / group;
-  const int64_t step = (int64_t)gridDim.x * groups;
+  const int64_t m = (int64_t)blockIdx.x * groups + g.id;
+  if (m >= p.M) return;  // whole groups
   auto has = [&](int i) { return FULL || g.tid + i * g.T < units; };
+  const int32_t* row = p.acc + m * p.H;
   int4 raw[NU][2];
-  float gx = 0.f;
-  auto load = [&](int64_t m) {
-    if (m >= p.M) return;
-    gx = __ldg(p.gammaX + m);
-    const int32_t* row = p.acc + m * p.H;
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      if (has(i)) {
-        const int64_t c = unit_column(g.tid + i * g.T);
-        raw[i][0] = __ldg(reinterpret_cast<const int4*>(row + c));
-        raw[i][1] = __ldg(reinterpret_cast<const int4*>(row + c + 32));
-      }
+  for (int i = 0; i < NU; ++i) {
+    if (has(i)) {
+      const int64_t c = unit_column(g.tid + i * g.T);
+      raw[i][0] = __ldg(reinterpret_cast<const int4*>(row + c));
+      raw[i][1] = __ldg(reinterpret_cast<const int4*>(row + c + 32));
     }
-  };
-  const float up = __ldg(p.g_up);
-  int64_t m = (int64_t)blockIdx.x * groups + g.id;
-  load(m);
-  for (; m < p.M; m += step) {
-    const float sc = __fdiv_rn(__fmul_rn(gx, up), 127.0f);
-    float v[NU][8], mx = 0.f;
+  }
+  const float sc = __fdiv_rn(__fmul_rn(__ldg(p.gammaX + m), __ldg(p.g_up)), 127.0f);
+  float v[NU][8], mx = 0.f;
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
+  for (int i = 0; i < NU; ++i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-      if (has(i)) {
-        const int e[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
-                          raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    if (has(i)) {
+      const int e[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
+                        raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = fmaxf(__fmul_rn((float)e[j], sc), 0.0f);
-      }
+      for (int j = 0; j < 8; ++j) v[i][j] = fmaxf(__fmul_rn((float)e[j], sc), 0.0f);
     }
-    load(m + step);
-    uint32_t w[NU][2];
-    const float sc8 = ckpt_codes<false, NU>(v, w);
+  }
+  uint32_t w[NU][2];
+  const float sc8 = ckpt_codes<false, NU>(v, w);
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      const int u = g.tid + i * g.T;
-      if (has(i)) {
-        store_unit_bytes(p.Pq + m * p.H, unit_column(u), w[i][0], w[i][1]);
-        if ((u & 7) == i) p.ps[(m * p.H + 8 * u) / 64] = sc8;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[i][j] = __fmul_rn(v[i][j], v[i][j]);
-        mx = fmaxf(mx, v[i][j]);
-      }
+  for (int i = 0; i < NU; ++i) {
+    const int u = g.tid + i * g.T;
+    if (has(i)) {
+      store_unit_bytes(p.Pq + m * p.H, unit_column(u), w[i][0], w[i][1]);
+      if ((u & 7) == i) p.ps[(m * p.H + 8 * u) / 64] = sc8;
     }
-    mx = group_reduce(g, mx, redf, [](float a, float b) { return fmaxf(a, b); });
-    const float s = __fdiv_rn(127.0f, __fadd_rn(mx, p.eps));
-    int sum = 0;
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      if (has(i)) {
-        uint32_t b[8];
+    for (int j = 0; j < 8; ++j) {
+      v[i][j] = __fmul_rn(v[i][j], v[i][j]);
+      mx = fmaxf(mx, v[i][j]);
+    }
+  }
+  mx = group_reduce(g, mx, redf, [](float a, float b) { return fmaxf(a, b); });
+  const float s = __fdiv_rn(127.0f, __fadd_rn(mx, p.eps));
+  int sum = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = token_bits(v[i][j], s);
-        const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
-        const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
-        sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
-        store_unit_bytes(p.Rq + m * p.H, unit_column(g.tid + i * g.T), w0, w1);
-      }
+  for (int i = 0; i < NU; ++i) {
+    if (has(i)) {
+      uint32_t b[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) b[j] = token_bits(v[i][j], s);
+      const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
+      const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
+      sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
+      store_unit_bytes(p.Rq + m * p.H, unit_column(g.tid + i * g.T), w0, w1);
     }
-    // also keeps the maxima from being written for the next row while they are read
-    sum = group_reduce(g, sum, redi, [](int a, int b) { return a + b; });
-    if (g.tid == 0) {
-      p.gammaR[m] = mx;
-      if (p.rowsum != nullptr) p.rowsum[m] = sum;
-    }
+  }
+  sum = group_reduce(g, sum, redi, [](int a, int b) { return a + b; });
+  if (g.tid == 0) {
+    p.gammaR[m] = mx;
+    if (p.rowsum != nullptr) p.rowsum[m] = sum;
   }
 }
 
-// Rows longer than a CTA's registers hold: the second pass reads them again.
+// Many rows, or rows longer than registers hold: the second pass reads them again.
 __global__ void __launch_bounds__(kNormThreads) relu2_requant_q8_long_kernel(const Relu2Params p) {
   __shared__ float redf[kNormThreads / 32];
   __shared__ int redi[kNormThreads / 32];
