@@ -471,7 +471,10 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
  *     in fixed point, rounded to 2^-23 of the largest of them or less (what
  *     aligning to it in an fp32 sum would lose); products and the sums of a
  *     group are exact integers, the rest is fp32. An infinity or NaN makes its
- *     token's results NaN. flags: BL_FLAG_PDL as for bl_linear_ex. */
+ *     token's results NaN. Above 5 tokens one launch makes the fixed-point
+ *     activations in the workspace (bl_linear_w4_workspace_bytes() bytes, 0 up
+ *     to 5 tokens) and the product reads them. flags: BL_FLAG_PDL as for
+ *     bl_linear_ex. */
 #define BL_W4_MAX_K 262144
 size_t bl_w4_bytes(int64_t N, int64_t K);
 int64_t bl_w4_scale_count(int64_t N, int64_t K, int group);
@@ -482,9 +485,11 @@ bl_status bl_pack_w4(const uint8_t* codes, const void* scales_in, const uint8_t*
                      bl_stream_t stream);
 bl_status bl_unpack_w4(const uint8_t* W4, const void* scales, const uint8_t* zeros, int64_t N,
                        int64_t K, int group, void* W, bl_dtype w_dtype, bl_stream_t stream);
+size_t bl_linear_w4_workspace_bytes(int64_t M, int64_t K, int group);
 bl_status bl_linear_w4(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, const uint8_t* W4,
                        const void* scales, const uint8_t* zeros, int64_t N, int group, void* Y,
-                       bl_dtype y_dtype, unsigned flags, bl_stream_t stream);
+                       bl_dtype y_dtype, void* workspace, size_t ws_bytes, unsigned flags,
+                       bl_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Layer norm in front of the activation quantiser, and its backward. The pages

@@ -628,17 +628,20 @@ def bl_unpack_w4(W4, scales, N: int, K: int, *, zeros=None, out_dtype=torch.floa
 
 @_placed
 def bl_linear_w4(X, W4, scales, N: int, *, zeros=None, out_dtype=torch.bfloat16, out=None,
-                 pdl=False):
+                 workspace=None, pdl=False):
     """Y [M, N] = X·Wᵀ for few tokens on 4-bit weights with group scales."""
-    st = _on(X=X, W4=W4, scales=scales, zeros=zeros, out=out)
+    st = _on(X=X, W4=W4, scales=scales, zeros=zeros, out=out, workspace=workspace)
     M, K = _matrix(X, "X")
     group = _check_w4(W4, scales, zeros, N, K)
     if out is None:
         out = X.new_empty((M, N), dtype=out_dtype)
     _shape(out, (M, N), "out")
-    check(load().bl_linear_w4(X.data_ptr(), _dt(X, "X"), M, K, W4.data_ptr(), scales.data_ptr(),
-                              _ptr(zeros), N, group, out.data_ptr(), _dt(out, "out"),
-                              BL_FLAG_PDL if pdl else 0, st), "bl_linear_w4")
+    L = load()
+    if workspace is None and M > 5:
+        workspace = _ws(int(L.bl_linear_w4_workspace_bytes(M, K, group)), X.device)
+    check(L.bl_linear_w4(X.data_ptr(), _dt(X, "X"), M, K, W4.data_ptr(), scales.data_ptr(),
+                         _ptr(zeros), N, group, out.data_ptr(), _dt(out, "out"), _ptr(workspace),
+                         _nbytes(workspace), BL_FLAG_PDL if pdl else 0, st), "bl_linear_w4")
     return out
 
 

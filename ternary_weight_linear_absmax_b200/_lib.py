@@ -87,8 +87,9 @@ SIGNATURES = {
     "bl_quant_weights_w4": (_int, [_vp, _int, _i64, _i64, _int, _vp, _vp, _vp, _vp]),
     "bl_pack_w4": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _vp]),
     "bl_unpack_w4": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _vp, _int, _vp]),
-    "bl_linear_w4": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _i64, _int, _vp, _int, _uint,
-                            _vp]),
+    "bl_linear_w4_workspace_bytes": (_sz, [_i64, _i64, _int]),
+    "bl_linear_w4": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _i64, _int, _vp, _int, _vp, _sz,
+                            _uint, _vp]),
     "bl_layernorm": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _f32, _vp, _int, _vp, _vp, _vp]),
     "bl_layernorm_quant": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _f32, _f32, _vp, _vp, _vp, _vp,
                                   _vp, _vp, _vp]),

@@ -879,7 +879,7 @@ inline unsigned loop_grid(int64_t items, int64_t per, int sms) {
 // One launch: slabs × clusters. Returns BL_ERR_SHAPE where the activations of
 // a pass do not fit.
 template <typename T, int V, int NT>
-bl_status launch_w4_nt(W4Params p, bool pdl, int dev, int sms, cudaStream_t st) {
+bl_status launch_w4_nt(W4Params p, uint8_t* workspace, bool pdl, int dev, int sms, cudaStream_t st) {
   using C = W4Pass<NT>;
   const int64_t RB = (p.N + 15) / 16, KB = (p.K + 127) / 128;
   const int toks = (int)(p.M < C::kTok ? p.M : C::kTok);
@@ -890,7 +890,7 @@ bl_status launch_w4_nt(W4Params p, bool pdl, int dev, int sms, cudaStream_t st) 
   int64_t slabs = 0;
   for (; ranks <= kW4MaxCluster; ranks *= 2) {
     const int64_t kb = (KB + ranks - 1) / ranks, out_rows = (int64_t)(kW4OutCap / (64 * toks));
-    if (3 * toks * kb * 128 > (int64_t)kW4SmemCap) continue;
+    if (kb * W4Record<V, NT>(toks).bytes > kW4SmemCap) continue;
     int64_t n = sms / ranks;
     if (n > RB) n = RB;
     if (ranks > 1 && n * out_rows < RB) n = (RB + out_rows - 1) / out_rows;
@@ -900,6 +900,22 @@ bl_status launch_w4_nt(W4Params p, bool pdl, int dev, int sms, cudaStream_t st) 
     break;
   }
   if (slabs == 0) return BL_ERR_SHAPE;
+  if constexpr (C::kPlanar) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((KB + 15) / 16), (unsigned)(p.M < 65535 ? p.M : 65535));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    auto* d = w4_digits_kernel<T, V, NT>;
+    BL_TRY(ensure_smem(d, dev, 0));
+    BL_CUDA(cudaLaunchKernelEx(&cfg, d, reinterpret_cast<const T*>(p.X), p.M, p.K, workspace));
+    p.digits = workspace;
+    pdl = true;  // the product may request its weights while the digits are made
+  }
   auto* k = w4_linear_kernel<T, V, NT>;
   BL_TRY(ensure_smem(k, dev, smem));
   p.slab_rows = (int)(RB / slabs);
@@ -927,28 +943,29 @@ bl_status launch_w4_nt(W4Params p, bool pdl, int dev, int sms, cudaStream_t st) 
   return BL_OK;
 }
 
+constexpr int64_t w4_part_tokens = 2 * 65535;
 // Tokens a launch takes at once: 2, 5, 8 or 16 per pass, fewer where the
 // activations of a pass do not fit.
 template <typename T, int V>
-bl_status launch_w4_v(const W4Params& p, bool pdl, int dev, int sms, cudaStream_t st) {
+bl_status launch_w4_v(const W4Params& p, uint8_t* ws, bool pdl, int dev, int sms, cudaStream_t st) {
   // grid.y holds 65,535 passes; longer calls go in parts
-  const int64_t part = 2 * 65535;
+  const int64_t part = w4_part_tokens;
   for (int64_t m = 0; m < p.M; m += part) {
     W4Params q = p;
     q.X = reinterpret_cast<const T*>(p.X) + m * p.K;
     q.Y = reinterpret_cast<uint8_t*>(p.Y) + m * p.N * (p.y_bf16 ? 2 : 4);
     q.M = p.M - m < part ? p.M - m : part;
     bl_status s = BL_ERR_SHAPE;
-    if (q.M > 8) s = launch_w4_nt<T, V, 6>(q, pdl, dev, sms, st);
-    if (q.M > 5 && s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 3>(q, pdl, dev, sms, st);
-    if (q.M > 2 && s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 2>(q, pdl, dev, sms, st);
-    if (s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 1>(q, pdl, dev, sms, st);
+    if (q.M > 8) s = launch_w4_nt<T, V, 6>(q, ws, pdl, dev, sms, st);
+    if (q.M > 5 && s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 3>(q, ws, pdl, dev, sms, st);
+    if (q.M > 2 && s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 2>(q, ws, pdl, dev, sms, st);
+    if (s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 1>(q, ws, pdl, dev, sms, st);
     if (s == BL_ERR_SHAPE && q.M > 1) {  // two long rows do not fit: one by one
       const int64_t M = q.M;
       q.M = 1;
       s = BL_OK;
       for (int64_t i = 0; i < M && s == BL_OK; ++i) {
-        s = launch_w4_nt<T, V, 1>(q, pdl, dev, sms, st);
+        s = launch_w4_nt<T, V, 1>(q, ws, pdl, dev, sms, st);
         q.X = reinterpret_cast<const T*>(q.X) + p.K;
         q.Y = reinterpret_cast<uint8_t*>(q.Y) + p.N * (p.y_bf16 ? 2 : 4);
       }
@@ -959,10 +976,11 @@ bl_status launch_w4_v(const W4Params& p, bool pdl, int dev, int sms, cudaStream_
 }
 
 template <typename T>
-bl_status launch_w4(const W4Params& p, int group, bool pdl, int dev, int sms, cudaStream_t st) {
-  if (group == 32) return launch_w4_v<T, 4>(p, pdl, dev, sms, st);
-  if (group == 64) return launch_w4_v<T, 2>(p, pdl, dev, sms, st);
-  return launch_w4_v<T, 1>(p, pdl, dev, sms, st);
+bl_status launch_w4(const W4Params& p, int group, uint8_t* ws, bool pdl, int dev, int sms,
+                    cudaStream_t st) {
+  if (group == 32) return launch_w4_v<T, 4>(p, ws, pdl, dev, sms, st);
+  if (group == 64) return launch_w4_v<T, 2>(p, ws, pdl, dev, sms, st);
+  return launch_w4_v<T, 1>(p, ws, pdl, dev, sms, st);
 }
 
 // --------------------------------------------------------------------------
@@ -2103,9 +2121,23 @@ bl_status bl_unpack_w4(const uint8_t* W4, const void* scales, const uint8_t* zer
   return BL_OK;
 }
 
+size_t bl_linear_w4_workspace_bytes(int64_t M, int64_t K, int group) {
+  if (M <= 5 || K <= 0 || check_group(group) != BL_OK) return 0;
+  // records of passes of 16 tokens or, where those do not fit, of 8: the
+  // larger of the two
+  const int64_t m = M < w4_part_tokens ? M : w4_part_tokens, KB = (K + 127) / 128;
+  auto bytes = [&](int64_t tok) {
+    const int64_t img = m < tok ? m : tok;
+    return (size_t)((m + tok - 1) / tok) * KB * (size_t)(img * 384 + (128 / group + 1) * tok * 4);
+  };
+  const size_t a = bytes(16), b = bytes(8);
+  return a > b ? a : b;
+}
+
 bl_status bl_linear_w4(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, const uint8_t* W4,
                        const void* scales, const uint8_t* zeros, int64_t N, int group, void* Y,
-                       bl_dtype y_dtype, unsigned flags, bl_stream_t stream) {
+                       bl_dtype y_dtype, void* workspace, size_t ws_bytes, unsigned flags,
+                       bl_stream_t stream) {
   BL_TRY(check_dtype(x_dtype));
   BL_TRY(check_dtype(y_dtype));
   BL_TRY(check_k(K));
@@ -2120,6 +2152,11 @@ bl_status bl_linear_w4(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, co
   BL_TRY(check_ptr(scales));
   if (zeros != nullptr) BL_TRY(check_ptr(zeros));
   BL_TRY(check_ptr(Y));
+  if (const size_t need = bl_linear_w4_workspace_bytes(M, K, group); need != 0) {
+    if (workspace == nullptr || ws_bytes < need) return BL_ERR_WORKSPACE;
+    BL_TRY(check_ptr(workspace));
+  }
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   int dev, sms;
   BL_TRY(current_device(&dev, &sms));
   W4Params p = {};
@@ -2134,8 +2171,8 @@ bl_status bl_linear_w4(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, co
   p.y_bf16 = y_dtype == BL_BF16;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool pdl = (flags & BL_FLAG_PDL) != 0;
-  return x_dtype == BL_BF16 ? launch_w4<__nv_bfloat16>(p, group, pdl, dev, sms, st)
-                            : launch_w4<float>(p, group, pdl, dev, sms, st);
+  return x_dtype == BL_BF16 ? launch_w4<__nv_bfloat16>(p, group, ws, pdl, dev, sms, st)
+                            : launch_w4<float>(p, group, ws, pdl, dev, sms, st);
 }
 
 // ---------------------------------------------------------------------------

@@ -31,6 +31,7 @@ struct W4Params {
   int64_t M, N, K;
   int y_bf16;
   int slab_rows, slab_more;       // row blocks per slab; the first slab_more have one more
+  const uint8_t* digits;          // records of w4_digits_kernel [pass][kb][record], or null
 };
 
 // d = A·B + c.
@@ -46,6 +47,9 @@ __device__ __forceinline__ void mma_u8s8_16832(int (&d)[4], uint32_t a0, uint32_
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -112,10 +116,22 @@ struct W4Smem {
   uint32_t part;   // float [warp][2][16][sums]: a run's first and last shares
   uint32_t ring;   // [warp][stage]: codes, scales, zero points
   uint32_t out;    // float [row block][token][16], in a cluster
-  uint32_t dsum;   // float [group][sum]: the activations' sums, in fixed point
-  uint32_t cf;     // float [block][sum]: what a digit, or 1 in fixed point, counts
-  uint32_t x;      // digits, [column][x_stride]
-  uint32_t x_stride, total;
+  uint32_t x;      // records of the CTA's K blocks
+  uint32_t total;
+};
+// The activations of 128 columns: the digits' MMA columns, 128 bytes each, the
+// fixed-point sums of the groups (float [group][sum]) and what a digit, or 1 in
+// fixed point, counts (float [sum]). A column's eight 16-byte pieces are
+// swapped in pairs in odd columns, so that two columns (the eight lanes of a
+// 16-byte read) fall on different banks.
+template <int V, int NT>
+struct W4Record {
+  uint32_t dsum, cf, bytes;
+  __host__ __device__ __forceinline__ explicit W4Record(int toks) {
+    dsum = 3 * toks * 128;
+    cf = dsum + V * W4Pass<NT>::kSums * 4;
+    bytes = cf + W4Pass<NT>::kSums * 4;
+  }
 };
 template <int V>
 __host__ __device__ constexpr int w4_stage_bytes() {
@@ -135,13 +151,8 @@ __host__ __device__ inline W4Smem w4_smem(int KB, int slab, int toks, int ranks)
   s.part = 0;
   s.ring = s.part + 2 * kW4Warps * 16 * C::kSums * 4;
   s.out = s.ring + kW4Warps * w4_stages<V>() * w4_stage_bytes<V>();
-  s.dsum = s.out + (ranks > 1 ? slab * toks * 64 : 0);
-  s.cf = s.dsum + KB * V * C::kSums * 4;
-  s.x = s.cf + KB * C::kSums * 4;
-  // 16 bytes more than the row: two columns (the eight lanes of a 16-byte
-  // read) then fall on different banks
-  s.x_stride = KB * 128 + 16;
-  s.total = s.x + 3 * toks * s.x_stride;
+  s.x = s.out + (ranks > 1 ? slab * toks * 64 : 0);
+  s.total = s.x + KB * W4Record<V, NT>(toks).bytes;
   return s;
 }
 
@@ -194,104 +205,135 @@ __device__ __forceinline__ void w4_store(const W4Params& p, int rb, int64_t m0, 
   }
 }
 
-// Activations of one CTA's K blocks into shared memory, as digits. Per token
-// and 128-column block: the largest power of two f with max|x|·f ≤ 127·2^16, then
-// x·f rounded to a 24-bit integer d2·2^16 + d1·2^8 + d0 with digits in
-// [−128, 127] (adding 0x808080 and flipping the same bits carries between
-// them), and what digit i counts, 2^(8i)/f. Sixteen lanes take a block, eight
-// columns each. The rounding, half of 1/f, is at most 2^-23 of the block's
-// largest value: what aligning to it in an fp32 sum would lose.
-template <typename T, int V, int NT, int B>
-__device__ __forceinline__ void w4_stage_x(uint8_t* smem, const W4Smem& L, const T* X, int64_t K,
-                                           int kb0, int KB, int toks) {
+// Eight activations of token m, columns 8·l .. 8·l + 7 of a 128-column block, into
+// the block's record, as digits; the sixteen lanes of a block (half a warp) call
+// together. f is the largest power of two with max|x|·f ≤ 127·2^16; x·f is
+// rounded to a 24-bit integer d2·2^16 + d1·2^8 + d0 with digits in [−128, 127]
+// (adding 0x808080 and flipping the same bits carries between them), and
+// digit i counts 2^(8i)/f. The rounding, half of 1/f, is at most 2^-23 of the
+// block's largest value: what aligning to it in an fp32 sum would lose.
+template <int V, int NT>
+__device__ __forceinline__ void w4_digits(const float (&v)[8], uint8_t* rec, const W4Record<V, NT>& R,
+                                          int m, bool write) {
   constexpr bool PL = W4Pass<NT>::kPlanar;
   constexpr int SUMS = W4Pass<NT>::kSums, GL = 16 / V;  // GL lanes per group
-  float* dsum = reinterpret_cast<float*>(smem + L.dsum);
-  float* cf = reinterpret_cast<float*>(smem + L.cf);
-  const int units = KB * 16, total = units * toks;
   const int l = threadIdx.x & 15;
+  uint32_t top = 0;  // largest magnitude, as bits: an infinity or NaN stays on top
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // f = 2^e, at most 2^125: a block below 1e-31 keeps fewer bits
+  const float f0 = __fdiv_rn(8323072.0f, fmaxf(__uint_as_float(top), 1e-31f));
+  const uint32_t fb = __float_as_uint(f0) & 0xFF800000u;
+  const float f = __uint_as_float(fb);
+  // 1/f, its exponent mirrored; an infinity or NaN makes the token's results NaN
+  const float unit = __uint_as_float(top < 0x7F800000u ? 0x7F000000u - fb : 0x7FFFFFFFu);
+  int fixed = 0;
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int n = __float2int_rn(__fmul_rn(v[j], f));
+    fixed += n;
+    w[j] = ((uint32_t)n + 0x808080u) ^ 0x808080u;
+  }
+#pragma unroll
+  for (int o = 1; o < GL; o <<= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
+  if (!write) return;
+#pragma unroll
+  for (int d = 0; d < 3; ++d) {  // digit d: byte d of the eight words
+    const uint32_t sel = d | ((4 + d) << 4);
+    const uint32_t a04 = __byte_perm(w[0], w[4], sel), a15 = __byte_perm(w[1], w[5], sel);
+    const uint32_t a26 = __byte_perm(w[2], w[6], sel), a37 = __byte_perm(w[3], w[7], sel);
+    const int xc = m * 3 + 2 - d;  // the highest digit first
+    // [t][u][8 bytes], t = l mod 4, u = l / 4
+    const uint32_t off = (((l & 3) * 2 + (l >> 3)) ^ (xc & 1)) * 16 + ((l >> 2) & 1) * 8;
+    *reinterpret_cast<uint2*>(rec + xc * 128 + off) =
+        make_uint2(__byte_perm(a04, a15, 0x5410), __byte_perm(a26, a37, 0x5410));
+  }
+  // The group's sum (|sum| ≤ 128·2^23) goes with the token, or with its lowest
+  // digit's column, which counts 1.
+  if (l % GL == 0) {
+    float* s = reinterpret_cast<float*>(rec + R.dsum) + (l / GL) * SUMS + (PL ? m : 3 * m);
+    if (!PL) s[0] = s[1] = 0.f;
+    s[PL ? 0 : 2] = (float)fixed;
+  }
+  if (l == 0) {
+    float* c = reinterpret_cast<float*>(rec + R.cf) + (PL ? m : 3 * m);
+    if (!PL) {
+      c[0] = __fmul_rn(unit, 65536.0f);
+      c[1] = __fmul_rn(unit, 256.0f);
+    }
+    c[PL ? 0 : 2] = unit;
+  }
+}
+
+// Eight activations as fp32, zeros where `in` is false.
+template <typename T>
+__device__ __forceinline__ void w4_load_x(const T* p, bool in, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  if (!in) return;
+  if constexpr (sizeof(T) == 2) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  } else {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 c = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = c.x; v[5] = c.y; v[6] = c.z; v[7] = c.w;
+  }
+}
+
+// A CTA's own activations into shared memory, B blocks' loads in flight
+// together.
+template <typename T, int V, int NT, int B>
+__device__ __forceinline__ void w4_stage_x(uint8_t* x, const W4Record<V, NT>& R, const T* X, int64_t K,
+                                           int kb0, int KB, int toks) {
+  const int units = KB * 16, total = units * toks;
   for (int i0 = threadIdx.x; i0 - (int)(threadIdx.x & 31) < total; i0 += B * kW4Threads) {
     float v[B][8];
     int tok[B], unit_of[B];
 #pragma unroll
-    for (int b = 0; b < B; ++b) {  // the loads of B blocks in flight together
+    for (int b = 0; b < B; ++b) {
       const int i = i0 + b * kW4Threads;
       tok[b] = toks == 1 ? 0 : i / units;
       unit_of[b] = i - tok[b] * units;
       const int64_t k = ((int64_t)kb0 * 16 + unit_of[b]) * 8;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[b][j] = 0.f;
-      if (i < total && k < K) {
-        const T* p = X + (int64_t)tok[b] * K + k;
-        if constexpr (sizeof(T) == 2) {
-          const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[b][2 * j] = __uint_as_float(w[j] << 16);
-            v[b][2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-          }
-        } else {
-          const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-          const float4 c = __ldg(reinterpret_cast<const float4*>(p) + 1);
-          v[b][0] = a.x; v[b][1] = a.y; v[b][2] = a.z; v[b][3] = a.w;
-          v[b][4] = c.x; v[b][5] = c.y; v[b][6] = c.z; v[b][7] = c.w;
-        }
-      }
+      w4_load_x(X + (int64_t)tok[b] * K + k, i < total && k < K, v[b]);
     }
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       const int i = i0 + b * kW4Threads;
       if (i - (int)(threadIdx.x & 31) >= total) break;  // the same for the warp
-      const int m = tok[b], kb = unit_of[b] >> 4;
-      uint32_t top = 0;  // largest magnitude, as bits: an infinity or NaN stays on top
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[b][j]) & 0x7FFFFFFFu);
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // f = 2^e, at most 2^125: a block below 1e-31 keeps fewer bits
-      const float f0 = __fdiv_rn(8323072.0f, fmaxf(__uint_as_float(top), 1e-31f));
-      const uint32_t fb = __float_as_uint(f0) & 0xFF800000u;
-      const float f = __uint_as_float(fb);
-      // 1/f, its exponent mirrored; an infinity or NaN makes the token's results NaN
-      const float unit = __uint_as_float(top < 0x7F800000u ? 0x7F000000u - fb : 0x7FFFFFFFu);
-      int fixed = 0;
-      uint32_t w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int n = __float2int_rn(__fmul_rn(v[b][j], f));
-        fixed += n;
-        w[j] = ((uint32_t)n + 0x808080u) ^ 0x808080u;
-      }
-#pragma unroll
-      for (int o = 1; o < GL; o <<= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
-      if (i < total) {
-        const uint32_t lane_off = kb * 128 + (l & 3) * 32 + (l >> 2) * 8;  // [t][u][8 bytes]
-#pragma unroll
-        for (int d = 0; d < 3; ++d) {  // digit d: byte d of the eight words
-          const uint32_t sel = d | ((4 + d) << 4);
-          const uint32_t a04 = __byte_perm(w[0], w[4], sel), a15 = __byte_perm(w[1], w[5], sel);
-          const uint32_t a26 = __byte_perm(w[2], w[6], sel), a37 = __byte_perm(w[3], w[7], sel);
-          *reinterpret_cast<uint2*>(smem + L.x + (m * 3 + 2 - d) * L.x_stride + lane_off) =
-              make_uint2(__byte_perm(a04, a15, 0x5410), __byte_perm(a26, a37, 0x5410));
-        }
-        // The group's sum (|sum| ≤ 128·2^23) goes with the token, or with its
-        // lowest digit's column, which counts 1.
-        if (l % GL == 0) {
-          float* s = dsum + (kb * V + l / GL) * SUMS + (PL ? m : 3 * m);
-          if (!PL) s[0] = s[1] = 0.f;
-          s[PL ? 0 : 2] = (float)fixed;
-        }
-        if (l == 0) {
-          float* c = cf + kb * SUMS + (PL ? m : 3 * m);
-          if (!PL) {
-            c[0] = __fmul_rn(unit, 65536.0f);
-            c[1] = __fmul_rn(unit, 256.0f);
-          }
-          c[PL ? 0 : 2] = unit;
-        }
-      }
+      w4_digits<V, NT>(v[b], x + (unit_of[b] >> 4) * R.bytes, R, tok[b], i < total);
     }
+  }
+}
+
+// The records of all tokens and blocks in global memory, [pass][kb][record]:
+// with more than a few tokens, making them again in every CTA would take longer
+// than the product. One warp per two blocks of a token (blockIdx.y and on).
+template <typename T, int V, int NT>
+__global__ void __launch_bounds__(256)
+w4_digits_kernel(const T* __restrict__ X, int64_t M, int64_t K, uint8_t* __restrict__ out) {
+  constexpr int TOK = W4Pass<NT>::kTok;
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  const int KB = (int)((K + 127) / 128), img = (int)min((int64_t)TOK, M);
+  const W4Record<V, NT> R(img);
+  const int kb = (int)(blockIdx.x * 16 + (threadIdx.x >> 4)), l = threadIdx.x & 15;
+  for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
+    const int64_t k = (int64_t)kb * 128 + 8 * l;
+    float v[8];
+    w4_load_x(X + m * K + k, k < K, v);
+    uint8_t* rec = out + ((m / TOK) * KB + kb) * (int64_t)R.bytes;
+    w4_digits<V, NT>(v, rec, R, (int)(m % TOK), kb < KB);
   }
 }
 
@@ -315,7 +357,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
   using C = W4Pass<NT>;
   constexpr int SUMS = C::kSums, TOK = C::kTok, ST = w4_stage_bytes<V>();
   constexpr int NA = SUMS / 8;                  // accumulator tiles
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   constexpr int D = w4_stages<V>();
@@ -363,11 +405,20 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
   for (int d = 0; d < D - 1; ++d) request(ring + d * ST);
   pdl_wait_prior_grid();
 
-  const T* X = reinterpret_cast<const T*>(p.X) + m0 * p.K;
-  if (KB * 16 * toks <= kW4Threads)
-    w4_stage_x<T, V, NT, 1>(smem, L, X, p.K, kb0, KB, toks);
-  else
-    w4_stage_x<T, V, NT, 4>(smem, L, X, p.K, kb0, KB, toks);
+  const int img = (int)min((int64_t)TOK, p.M);
+  const W4Record<V, NT> R(img);
+  uint8_t* x = smem + L.x;
+  if constexpr (C::kPlanar) {
+    const uint8_t* rec = p.digits + ((int64_t)blockIdx.y * KBt + kb0) * R.bytes;
+    for (uint32_t i = 16 * tid; i < KB * R.bytes; i += 16 * kW4Threads) cp_async16(smem_u32(x) + i, rec + i);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    const T* X = reinterpret_cast<const T*>(p.X) + m0 * p.K;
+    if (KB * 16 * toks <= kW4Threads)
+      w4_stage_x<T, V, NT, 1>(x, R, X, p.K, kb0, KB, toks);
+    else
+      w4_stage_x<T, V, NT, 4>(x, R, X, p.K, kb0, KB, toks);
+  }
   if (it0 == it1)  // fewer blocks than warps: an empty run adds nothing
     for (int j = lane; j < 16 * SUMS; j += 32) part[warp * 32 * SUMS + j] = 0.f;
   __syncthreads();
@@ -382,9 +433,9 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
       xc = (8 * (n / 3) + g) % toks * 3 + n % 3;
     else
       xc = (8 * n + g) % (3 * toks);
-    xaddr[n] = smem_u32(smem) + L.x + xc * L.x_stride + 32 * t;
+    xaddr[n] = smem_u32(x) + xc * 128 + 16 * ((2 * t) ^ (xc & 1));
   }
-  const uint32_t dsum = smem_u32(smem) + L.dsum + 8 * t, cf = smem_u32(smem) + L.cf + 8 * t;
+  const uint32_t dsum = smem_u32(x) + R.dsum + 8 * t, cf = smem_u32(x) + R.cf + 8 * t;
   const bool zs = p.zeros != nullptr;
   const int magic[4] = {0x4B400000, 0x4B400000, 0x4B400000, 0x4B400000};
 
@@ -395,7 +446,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
     float acc[NA][4];
 #pragma unroll
     for (int n = 0; n < NA; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-    uint32_t x_off = kb * 128, ds_at = dsum + kb * (V * SUMS * 4), cf_at = cf + kb * (SUMS * 4);
+    uint32_t x_off = kb * R.bytes;
     for (; kb < end; ++kb) {
       // D − 1 blocks are under way; the oldest is next. Past the barrier every
       // lane sees it and is done with the stage before it, which is filled anew.
@@ -433,7 +484,8 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
 #pragma unroll
         for (int j = 0; j < ND; ++j) {
           const int tile = n * ND + j;
-          const uint4 x0 = lds128(xaddr[tile] + x_off), x1 = lds128(xaddr[tile] + x_off + 16);
+          const uint32_t at = xaddr[tile] + x_off;  // the other piece of the pair is 16 bytes off
+          const uint4 x0 = lds128(at), x1 = lds128(at ^ 16u);
           const uint32_t b[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
           for (int v = 0; v < V; ++v) {
@@ -446,11 +498,11 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
             }
           }
         }
-        const uint2 cq = lds64(cf_at + 32 * n);
+        const uint2 cq = lds64(cf + x_off + 32 * n);
         const float c0 = __uint_as_float(cq.x), c1 = __uint_as_float(cq.y);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const uint2 dq = lds64(ds_at + (v * SUMS + 8 * n) * 4);
+          const uint2 dq = lds64(dsum + x_off + (v * SUMS + 8 * n) * 4);
           const float t0 = __uint_as_float(dq.x), t1 = __uint_as_float(dq.y);
           float y[4];
 #pragma unroll
@@ -466,9 +518,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
           acc[n][3] = fmaf(fmaf(z1[v], t1, y[3]), s1[v] * c1, acc[n][3]);
         }
       }
-      x_off += 128;
-      ds_at += V * SUMS * 4;
-      cf_at += SUMS * 4;
+      x_off += R.bytes;
       last = src;
       src = src == ring + (D - 1) * ST ? ring : src + ST;
     }

@@ -53,18 +53,24 @@ def test_w4_refusals(lib, p):
     assert u(p, p, None, 16, 63, 32, p, 0, None) == BAD_SHAPE
     assert u(p, p, None, 16, 64, 32, None, 0, None) == BAD_ARG
     f = lib.bl_linear_w4
-    assert f(p, 1, 1, 64, p, p, None, 16, 96, p, 1, 0, None) == BAD_SHAPE
-    assert f(p, 1, 1, 96, p, p, None, 16, 32, p, 1, 0, None) == BAD_SHAPE
-    assert f(p, 1, 1, (1 << 22) + 64, p, p, None, 16, 32, p, 1, 0, None) == BAD_SHAPE
-    assert f(p, 1, 1, 262144 + 64, p, p, None, 16, 32, p, 1, 0, None) == BAD_SHAPE
-    assert f(None, 1, 0, 262144, None, None, None, 16, 32, None, 1, 0, None) == 0
-    assert f(p, 1, -1, 64, p, p, None, 16, 32, p, 1, 0, None) == BAD_SHAPE
-    assert f(p, 2, 1, 64, p, p, None, 16, 32, p, 1, 0, None) == BAD_DTYPE
-    assert f(p, 1, 1, 64, p, p, None, 16, 32, p, 1, 2, None) == BAD_ARG    # BL_FLAG_RAW_I32
-    assert f(p + 2, 1, 1, 64, p, p, None, 16, 32, p, 1, 0, None) == BAD_ALIGN
-    assert f(p, 1, 1, 64, p, p, None, 16, 32, None, 1, 0, None) == BAD_ARG
-    assert f(None, 1, 0, 64, None, None, None, 16, 32, None, 1, 0, None) == 0
-    assert f(None, 1, 1, 64, None, None, None, 0, 32, None, 1, 0, None) == 0
+    assert lib.bl_linear_w4_workspace_bytes(5, 64, 32) == 0
+    assert lib.bl_linear_w4_workspace_bytes(6, 128, 128) >= 6 * 3 * 128
+    assert lib.bl_linear_w4_workspace_bytes(17, 128, 128) >= 2 * 16 * 3 * 128
+    assert f(p, 1, 6, 64, p, p, None, 16, 32, p, 1, None, 0, 0, None) == BAD_WS
+    assert f(p, 1, 6, 64, p, p, None, 16, 32, p, 1, p, 64, 0, None) == BAD_WS
+    assert f(p, 1, 6, 64, p, p, None, 16, 32, p, 1, p + 8, 1 << 20, 0, None) == BAD_ALIGN
+    assert f(p, 1, 1, 64, p, p, None, 16, 96, p, 1, None, 0, 0, None) == BAD_SHAPE
+    assert f(p, 1, 1, 96, p, p, None, 16, 32, p, 1, None, 0, 0, None) == BAD_SHAPE
+    assert f(p, 1, 1, (1 << 22) + 64, p, p, None, 16, 32, p, 1, None, 0, 0, None) == BAD_SHAPE
+    assert f(p, 1, 1, 262144 + 64, p, p, None, 16, 32, p, 1, None, 0, 0, None) == BAD_SHAPE
+    assert f(None, 1, 0, 262144, None, None, None, 16, 32, None, 1, None, 0, 0, None) == 0
+    assert f(p, 1, -1, 64, p, p, None, 16, 32, p, 1, None, 0, 0, None) == BAD_SHAPE
+    assert f(p, 2, 1, 64, p, p, None, 16, 32, p, 1, None, 0, 0, None) == BAD_DTYPE
+    assert f(p, 1, 1, 64, p, p, None, 16, 32, p, 1, None, 0, 2, None) == BAD_ARG    # BL_FLAG_RAW_I32
+    assert f(p + 2, 1, 1, 64, p, p, None, 16, 32, p, 1, None, 0, 0, None) == BAD_ALIGN
+    assert f(p, 1, 1, 64, p, p, None, 16, 32, None, 1, None, 0, 0, None) == BAD_ARG
+    assert f(None, 1, 0, 64, None, None, None, 16, 32, None, 1, None, 0, 0, None) == 0
+    assert f(None, 1, 1, 64, None, None, None, 0, 32, None, 1, None, 0, 0, None) == 0
 
 
 def test_norm_refusals(lib, p):
