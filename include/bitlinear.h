@@ -536,7 +536,7 @@ bl_status bl_layernorm_grad_q8(const void* dY, bl_dtype dy_dtype, const int8_t* 
  *     h = acc·((gamma_x·gamma_up)/127), p = max(h, 0), r = p² (fp32); the tokens
  *     R_q [M, H], gamma_r [M] and rowsum [M] (may be NULL) of the down-projection,
  *     as in bl_ffn_relu2, and the unsigned checkpoint of p (P_q [M, H] bytes,
- *     p_scale [M, H/64]).
+ *     p_scale [M, H/64]; both NULL: not kept).
  *   bl_relu2_grad_q8     dH [M, H] = 2·p̂·dR, p̂ = p_scale·P_q; dR fp32/bf16, dH
  *     fp32/bf16 (bf16 is what bl_ste_grad_weight / _input take without a copy). */
 bl_status bl_relu2_requant_q8(const int32_t* acc_up, const float* gamma_x, const float* gamma_up,

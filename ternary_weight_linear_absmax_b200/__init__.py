@@ -730,10 +730,11 @@ def bl_layernorm_grad_q8(dY, xhat_q, xhat_scale, rstd, weight, *, out_dtype=torc
 
 
 @_placed
-def bl_relu2_requant_q8(acc_up, gamma_x, gamma_up, eps: float = 1e-5):
-    """ReLU² of the FFN in training, from the up-projection's INT32 accumulators:
-    (R_q int8 [M, H], γ_r fp32 [M], Σ R_q int32 [M], and the 8-bit checkpoint of
-    max(h, 0): uint8 [M, H], fp32 [M, H/64])."""
+def bl_relu2_requant_q8(acc_up, gamma_x, gamma_up, eps: float = 1e-5, *, checkpoint: bool = True):
+    """ReLU² of the FFN, from the up-projection's INT32 accumulators: (R_q int8
+    [M, H], γ_r fp32 [M], Σ R_q int32 [M], and the 8-bit checkpoint of
+    max(h, 0): uint8 [M, H], fp32 [M, H/64], or None twice without
+    ``checkpoint``)."""
     st = _on(acc_up=acc_up, gamma_x=gamma_x, gamma_up=gamma_up)
     M, H = _matrix(acc_up, "acc_up")
     _of(acc_up, torch.int32, (M, H), "acc_up")
@@ -742,11 +743,11 @@ def bl_relu2_requant_q8(acc_up, gamma_x, gamma_up, eps: float = 1e-5):
     R_q = acc_up.new_empty((M, H), dtype=torch.int8)
     gamma_r = acc_up.new_empty((M,), dtype=torch.float32)
     rowsum = acc_up.new_empty((M,), dtype=torch.int32)
-    P_q = acc_up.new_empty((M, H), dtype=torch.uint8)
-    p_scale = acc_up.new_empty((M, H // 64), dtype=torch.float32)
+    P_q = acc_up.new_empty((M, H), dtype=torch.uint8) if checkpoint else None
+    p_scale = acc_up.new_empty((M, H // 64), dtype=torch.float32) if checkpoint else None
     check(load().bl_relu2_requant_q8(acc_up.data_ptr(), gamma_x.data_ptr(), gamma_up.data_ptr(),
                                      M, H, float(eps), R_q.data_ptr(), gamma_r.data_ptr(),
-                                     rowsum.data_ptr(), P_q.data_ptr(), p_scale.data_ptr(), st),
+                                     rowsum.data_ptr(), _ptr(P_q), _ptr(p_scale), st),
           "bl_relu2_requant_q8")
     return R_q, gamma_r, rowsum, P_q, p_scale
 

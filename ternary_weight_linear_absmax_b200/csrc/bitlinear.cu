@@ -2281,6 +2281,7 @@ bl_status bl_relu2_requant_q8(const int32_t* acc_up, const float* gamma_x, const
   BL_TRY(check_k(H));
   BL_TRY(check_rows(M));
   BL_TRY(check_eps(eps));
+  if ((P_q == nullptr) != (p_scale == nullptr)) return BL_ERR_INVALID_ARG;
   if (M == 0) return BL_OK;
   BL_TRY(check_ptr(acc_up));
   BL_TRY(check_ptr(gamma_x));
@@ -2288,8 +2289,10 @@ bl_status bl_relu2_requant_q8(const int32_t* acc_up, const float* gamma_x, const
   BL_TRY(check_ptr(R_q));
   BL_TRY(check_ptr(gamma_r));
   if (rowsum != nullptr) BL_TRY(check_ptr(rowsum));
-  BL_TRY(check_ptr(P_q));
-  BL_TRY(check_ptr(p_scale));
+  if (P_q != nullptr) {
+    BL_TRY(check_ptr(P_q));
+    BL_TRY(check_ptr(p_scale));
+  }
   int dev, sms;
   BL_TRY(current_device(&dev, &sms));
   const Relu2Params p = {acc_up, gamma_x, gamma_up, M, H, eps, R_q, gamma_r, rowsum, P_q, p_scale};
@@ -2301,8 +2304,10 @@ bl_status bl_relu2_requant_q8(const int32_t* acc_up, const float* gamma_x, const
     launch_relu2<2>(p, s.group, sms, st);
   else if (s.nu == 4)
     launch_relu2<4>(p, s.group, sms, st);
+  else if (P_q != nullptr)
+    relu2_requant_q8_long_kernel<true><<<(unsigned)M, kNormThreads, 0, st>>>(p);
   else
-    relu2_requant_q8_long_kernel<<<(unsigned)M, kNormThreads, 0, st>>>(p);
+    relu2_requant_q8_long_kernel<false><<<(unsigned)M, kNormThreads, 0, st>>>(p);
   BL_CUDA(cudaGetLastError());
   return BL_OK;
 }

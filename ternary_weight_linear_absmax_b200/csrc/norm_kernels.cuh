@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
   if constexpr (sizeof(OUT) > 1) {
     for (int64_t u = threadIdx.x; u < units; u += kNormThreads) {
       load_unit(row, unit_column(u), x);
+#pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = __fsub_rn(x[j], mean);
       norm_affine_unit(x, rstd, p.weight, p.bias, unit_column(u), xhat, y);
       store_unit(reinterpret_cast<OUT*>(p.Y) + m * p.K, unit_column(u), y);
@@ -480,8 +481,9 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
       for (int j = 0; j < 8; ++j) xhat[j] = 0.f;
       if (u < units) {
         load_unit(row, unit_column(u), x);
+#pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = __fsub_rn(x[j], mean);
-      norm_affine_unit(x, rstd, p.weight, p.bias, unit_column(u), xhat, y);
+        norm_affine_unit(x, rstd, p.weight, p.bias, unit_column(u), xhat, y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(y[j]));
       }
@@ -499,6 +501,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
     int sum = 0;
     for (int64_t u = threadIdx.x; u < units; u += kNormThreads) {
       load_unit(row, unit_column(u), x);
+#pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = __fsub_rn(x[j], mean);
       norm_affine_unit(x, rstd, p.weight, p.bias, unit_column(u), xhat, y);
       uint32_t b[8];
@@ -877,7 +880,7 @@ struct Relu2Params {
   int8_t* Rq;           // [M, H]
   float* gammaR;        // [M]
   int32_t* rowsum;      // [M] or null
-  uint8_t* Pq;          // [M, H]
+  uint8_t* Pq;          // [M, H] or null
   float* ps;            // [M, H/64]
 };
 
@@ -913,15 +916,20 @@ __global__ void __launch_bounds__(512, 2) relu2_requant_q8_kernel(const Relu2Par
       for (int j = 0; j < 8; ++j) v[i][j] = fmaxf(__fmul_rn((float)e[j], sc), 0.0f);
     }
   }
-  uint32_t w[NU][2];
-  const float sc8 = ckpt_codes<false, NU>(v, w);
+  if (p.Pq != nullptr) {
+    uint32_t w[NU][2];
+    const float sc8 = ckpt_codes<false, NU>(v, w);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int u = g.tid + i * g.T;
+      if (has(i)) {
+        store_unit_bytes(p.Pq + m * p.H, unit_column(u), w[i][0], w[i][1]);
+        if ((u & 7) == i) p.ps[(m * p.H + 8 * u) / 64] = sc8;
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int u = g.tid + i * g.T;
-    if (has(i)) {
-      store_unit_bytes(p.Pq + m * p.H, unit_column(u), w[i][0], w[i][1]);
-      if ((u & 7) == i) p.ps[(m * p.H + 8 * u) / 64] = sc8;
-    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       v[i][j] = __fmul_rn(v[i][j], v[i][j]);
@@ -951,6 +959,7 @@ __global__ void __launch_bounds__(512, 2) relu2_requant_q8_kernel(const Relu2Par
 }
 
 // Many rows, or rows longer than registers hold: the second pass reads them again.
+template <bool KEEP>
 __global__ void __launch_bounds__(kNormThreads) relu2_requant_q8_long_kernel(const Relu2Params p) {
   __shared__ float redf[kNormThreads / 32];
   __shared__ int redi[kNormThreads / 32];
@@ -970,11 +979,13 @@ __global__ void __launch_bounds__(kNormThreads) relu2_requant_q8_long_kernel(con
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
     if (u < units) load_p(u, v);
-    uint32_t w0, w1;
-    const float s = ckpt_codes8<false>(v, w0, w1);
-    if (u < units) {
-      store_unit_bytes(p.Pq + m * p.H, unit_column(u), w0, w1);
-      if ((u & 7) == 0) p.ps[(m * p.H + 8 * u) / 64] = s;
+    if constexpr (KEEP) {
+      uint32_t w0, w1;
+      const float s = ckpt_codes8<false>(v, w0, w1);
+      if (u < units) {
+        store_unit_bytes(p.Pq + m * p.H, unit_column(u), w0, w1);
+        if ((u & 7) == 0) p.ps[(m * p.H + 8 * u) / 64] = s;
+      }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) mx = fmaxf(mx, __fmul_rn(v[j], v[j]));

@@ -105,6 +105,7 @@ def test_relu2_refusals(lib, p):
     assert f(p, p, p, 1, 64, -1.0, p, p, p, p, p, None) == BAD_ARG
     assert f(p, p, None, 1, 64, 1e-5, p, p, p, p, p, None) == BAD_ARG
     assert f(p, p, p, 1, 64, 1e-5, p, p, p, p + 1, p, None) == BAD_ALIGN
+    assert f(p, p, p, 1, 64, 1e-5, p, p, p, p, None, None) == BAD_ARG      # half a checkpoint
     assert f(None, None, None, 0, 64, 1e-5, None, None, None, None, None, None) == 0
     g = lib.bl_relu2_grad_q8
     assert g(p, 0, p, p, 1, 32, p, 1, None) == BAD_SHAPE
