@@ -540,9 +540,8 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
           w4_store(p, rb0 + rb, m0, j, y);
       }
       __syncwarp();
-    } else {
-      slot = 1;
     }
+    slot = 1;
     kb = 0;
     ++rb;
   }

@@ -121,6 +121,17 @@ def test_linear_long(bl, M, N, K, group):
     _check(bl, M, N, K, group, True, "bf16", "f32", seed=K)
 
 
+@pytest.mark.parametrize("M,N,K,group", [(1, 60000, 128, 128), (3, 50000, 256, 64), (2, 47360, 384, 32),
+                                         (5, 128256, 192, 64), (7, 80000, 256, 128), (16, 40000, 320, 32)])
+def test_linear_runs_of_whole_row_blocks(bl, M, N, K, group):
+    """Short rows, many of them: a warp's run holds whole row blocks between
+    the ones that it shares with its neighbours. Twice, with another call's
+    leftovers in shared memory between."""
+    _check(bl, M, N, K, group, False, "bf16", "f32", seed=N)
+    _check(bl, 4, 1000, 2048, 32, True, "f32", "f32", seed=1)
+    _check(bl, M, N, K, group, True, "f32", "bf16", seed=N + 1)
+
+
 def test_linear_seeded_shapes(bl):
     rng = np.random.default_rng(7)
     for i in range(24):
