@@ -1086,7 +1086,8 @@ bl_status launch_norm_grad_nu(const NormGradParams& p, int grid, int dev, cudaSt
   size_t smem = (size_t)stage * stages;
   const size_t share = (size_t)groups * 2 * p.K * 4;
   if (smem < share) smem = share;
-  auto* k = layernorm_grad_kernel<TD, TX, TO, NU>;
+  auto* k = units == (int64_t)group * NU ? layernorm_grad_kernel<TD, TX, TO, NU, true>
+                                         : layernorm_grad_kernel<TD, TX, TO, NU, false>;
   BL_TRY(ensure_smem(k, dev, smem));
   k<<<grid, groups * group, smem, st>>>(p, group, stages);
   BL_CUDA(cudaGetLastError());

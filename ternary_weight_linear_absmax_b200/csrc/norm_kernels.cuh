@@ -248,6 +248,11 @@ struct RowGroup {
   int T, id, tid, warps;  // threads, which group, thread in it, its warps
   __device__ __forceinline__ explicit RowGroup(int t)
       : T(t), id((int)threadIdx.x / t), tid((int)threadIdx.x % t), warps(t >> 5) {}
+  // First of the thread's units when each warp of the group takes 32·nu units in
+  // a row; the others follow 32 apart, at distances known to the compiler.
+  __device__ __forceinline__ int first_unit(int nu) const {
+    return (tid >> 5) * 32 * nu + (tid & 31);
+  }
   __device__ __forceinline__ void sync() const {
     if (T == 32)
       __syncwarp();
@@ -328,14 +333,15 @@ __global__ void __launch_bounds__(norm_threads(NU)) layernorm_kernel(const NormP
   const int units = (int)(p.K / 8), groups = (int)blockDim.x / group;
   const int64_t step = (int64_t)gridDim.x * groups;
   auto add = [](auto a, auto b) { return a + b; };
-  auto has = [&](int i) { return FULL || g.tid + i * g.T < units; };
+  const int u0 = g.first_unit(NU);
+  auto has = [&](int i) { return FULL || u0 + 32 * i < units; };
   RawUnit<T> raw[NU];
   auto load = [&](int64_t m) {
     if (m >= p.M) return;
     const T* row = reinterpret_cast<const T*>(p.X) + m * p.K;
 #pragma unroll
     for (int i = 0; i < NU; ++i)
-      if (has(i)) raw[i].load(row, unit_column(g.tid + i * g.T));
+      if (has(i)) raw[i].load(row, unit_column(u0 + 32 * i));
   };
   int64_t m = (int64_t)blockIdx.x * groups + g.id;
   load(m);
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(norm_threads(NU)) layernorm_kernel(const NormP
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         if (has(i)) {
-          const int64_t c = unit_column(g.tid + i * g.T);
+          const int64_t c = unit_column(u0 + 32 * i);
           norm_affine_unit(v[i], rstd, p.weight, p.bias, c, xhat, v[i]);
           store_unit(reinterpret_cast<OUT*>(p.Y) + m * p.K, c, v[i]);
         }
@@ -394,7 +400,7 @@ __global__ void __launch_bounds__(norm_threads(NU)) layernorm_kernel(const NormP
         const float sc = ckpt_codes<true, NU>(v, w);
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-          const int u = g.tid + i * g.T;
+          const int u = u0 + 32 * i;
           if (has(i)) {
             store_unit_bytes(p.xq + m * p.K, unit_column(u), w[i][0], w[i][1]);
             if ((u & 7) == i) p.xs[(m * p.K + 8 * u) / 64] = sc;
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(norm_threads(NU)) layernorm_kernel(const NormP
       for (int i = 0; i < NU; ++i) {
         if (has(i)) {
           norm_affine_unit(v[i], p.xq != nullptr ? 1.0f : rstd, p.weight, p.bias,
-                           unit_column(g.tid + i * g.T), xhat, v[i]);
+                           unit_column(u0 + 32 * i), xhat, v[i]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[i][j]));
         }
@@ -422,7 +428,7 @@ __global__ void __launch_bounds__(norm_threads(NU)) layernorm_kernel(const NormP
           const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
           const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
           sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
-          store_unit_bytes(p.Aq + m * p.K, unit_column(g.tid + i * g.T), w0, w1);
+          store_unit_bytes(p.Aq + m * p.K, unit_column(u0 + 32 * i), w0, w1);
         }
       }
       if (p.rowsum != nullptr) sum = group_reduce(g, sum, redi, add);
@@ -620,7 +626,7 @@ __host__ __device__ constexpr int norm_stage_bytes(int T) {
 // and keeps their shares of dw and db in registers; the two row sums are the
 // only thing that the group exchanges. The CTA's groups add up their shares in
 // shared memory at the end.
-template <typename TD, typename TX, typename TO, int NU>
+template <typename TD, typename TX, typename TO, int NU, bool FULL>
 __global__ void __launch_bounds__(kNormGradThreads<NU>)
 layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -630,20 +636,22 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
   constexpr int BD = 4 * sizeof(TD), BX = 4 * sizeof(TX);  // bytes of a piece
   const int stage_bytes = norm_stage_bytes<TD, TX, NU>(T);
   const uint32_t ring = smem_u32(smem) + g.id * stages * stage_bytes;
-  const uint32_t mine_d = ring + BD * g.tid, mine_x = ring + NU * T * BD + BX * g.tid;
+  const int u0 = g.first_unit(NU);
+  auto has = [&](int i) { return FULL || u0 + 32 * i < units; };
+  const uint32_t mine_d = ring + BD * u0, mine_x = ring + NU * T * BD + BX * u0;
   const int64_t step = (int64_t)gridDim.x * groups;
   int64_t next = (int64_t)g.id * gridDim.x + blockIdx.x;  // the next row to request
   const int64_t first = next;
   int q = 0;
   auto request = [&]() {
     if (next < p.M) {
-      const TD* d = reinterpret_cast<const TD*>(p.dY) + next * p.K + 4 * g.tid;
-      const TX* x = reinterpret_cast<const TX*>(p.X) + next * p.K + 4 * g.tid;
+      const TD* d = reinterpret_cast<const TD*>(p.dY) + next * p.K + 4 * u0;
+      const TX* x = reinterpret_cast<const TX*>(p.X) + next * p.K + 4 * u0;
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
-        if (g.tid + i * T < units) {
-          cp_async<BD>(mine_d + q * stage_bytes + i * T * BD, d + 4 * i * T);
-          cp_async<BX>(mine_x + q * stage_bytes + i * T * BX, x + 4 * i * T);
+        if (has(i)) {
+          cp_async<BD>(mine_d + q * stage_bytes + 32 * i * BD, d + 128 * i);
+          cp_async<BX>(mine_x + q * stage_bytes + 32 * i * BX, x + 128 * i);
         }
       }
     }
@@ -656,14 +664,13 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
   float dw[NU][4], db[NU][4], w[NU][4];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int u = g.tid + i * T;
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = w[i][j] = 0.f;
-    if (NU < 8 && u < units) norm_load4(p.weight + 4 * u, w[i]);
+    if (NU < 8 && has(i)) norm_load4(p.weight + 4 * u0 + 128 * i, w[i]);
   }
   auto get = [&](int stage, int i, float mean, float rstd, float xs, float (&dy)[4], float (&xh)[4]) {
-    lds4<TD>(mine_d + stage * stage_bytes + i * T * BD, dy);
-    lds4<TX>(mine_x + stage * stage_bytes + i * T * BX, xh);
+    lds4<TD>(mine_d + stage * stage_bytes + 32 * i * BD, dy);
+    lds4<TX>(mine_x + stage * stage_bytes + 32 * i * BX, xh);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       xh[j] = sizeof(TX) == 1 ? __fmul_rn(xh[j], xs) : __fmul_rn(__fsub_rn(xh[j], mean), rstd);
@@ -679,7 +686,7 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
     if constexpr (sizeof(TX) > 1) mean_n = __ldg(p.mean + m);
 #pragma unroll
     for (int i = 0; i < NU; ++i)
-      if (sizeof(TX) == 1 && g.tid + i * T < units) xs_n[i] = __ldg(p.xs + (m * units + g.tid + i * T) / 16);
+      if (sizeof(TX) == 1 && has(i)) xs_n[i] = __ldg(p.xs + m * (units / 16) + u0 / 16 + 2 * i);
   };
 #pragma unroll
   for (int i = 0; i < NU; ++i) xs_n[i] = 0.f;
@@ -702,10 +709,9 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
     float a = 0.f, b = 0.f;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const int u = g.tid + i * T;
-      if (u < units) {
+      if (has(i)) {
         get(stage, i, mean, rstd, xs[i], dy[i], xh[i]);
-        if (NU == 8) norm_load4(p.weight + 4 * u, w[i]);
+        if (NU == 8) norm_load4(p.weight + 4 * u0 + 128 * i, w[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           dw[i][j] = fmaf(dy[i][j], xh[i][j], dw[i][j]);
@@ -732,16 +738,15 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
     b *= inv_k;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const int u = g.tid + i * T;
-      if (u < units) {
+      if (has(i)) {
         if (NU == 8) {  // read again rather than kept
           get(stage, i, mean, rstd, xs[i], dy[i], xh[i]);
-          norm_load4(p.weight + 4 * u, w[i]);
+          norm_load4(p.weight + 4 * u0 + 128 * i, w[i]);
         }
         float dx[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) dx[j] = rstd * fmaf(-xh[i][j], b, fmaf(dy[i][j], w[i][j], -a));
-        store4(reinterpret_cast<TO*>(p.dX) + m * p.K + 4 * u, dx);
+        store4(reinterpret_cast<TO*>(p.dX) + m * p.K + 4 * u0 + 128 * i, dx);
       }
     }
     stage = stage + 1 == stages ? 0 : stage + 1;
@@ -752,10 +757,9 @@ layernorm_grad_kernel(const NormGradParams p, int group, int stages) {
   float* share = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int u = g.tid + i * T;
-    if (u < units) {
-      store4(share + (int64_t)g.id * 2 * p.K + 4 * u, dw[i]);
-      store4(share + (int64_t)g.id * 2 * p.K + p.K + 4 * u, db[i]);
+    if (has(i)) {
+      store4(share + (int64_t)g.id * 2 * p.K + 4 * u0 + 128 * i, dw[i]);
+      store4(share + (int64_t)g.id * 2 * p.K + p.K + 4 * u0 + 128 * i, db[i]);
     }
   }
   __syncthreads();
@@ -892,13 +896,14 @@ __global__ void __launch_bounds__(512, 2) relu2_requant_q8_kernel(const Relu2Par
   const int units = (int)(p.H / 8), groups = (int)blockDim.x / group;
   const int64_t m = (int64_t)blockIdx.x * groups + g.id;
   if (m >= p.M) return;  // whole groups
-  auto has = [&](int i) { return FULL || g.tid + i * g.T < units; };
+  const int u0 = g.first_unit(NU);
+  auto has = [&](int i) { return FULL || u0 + 32 * i < units; };
   const int32_t* row = p.acc + m * p.H;
   int4 raw[NU][2];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     if (has(i)) {
-      const int64_t c = unit_column(g.tid + i * g.T);
+      const int64_t c = unit_column(u0 + 32 * i);
       raw[i][0] = __ldg(reinterpret_cast<const int4*>(row + c));
       raw[i][1] = __ldg(reinterpret_cast<const int4*>(row + c + 32));
     }
@@ -921,7 +926,7 @@ __global__ void __launch_bounds__(512, 2) relu2_requant_q8_kernel(const Relu2Par
     const float sc8 = ckpt_codes<false, NU>(v, w);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const int u = g.tid + i * g.T;
+      const int u = u0 + 32 * i;
       if (has(i)) {
         store_unit_bytes(p.Pq + m * p.H, unit_column(u), w[i][0], w[i][1]);
         if ((u & 7) == i) p.ps[(m * p.H + 8 * u) / 64] = sc8;
@@ -948,7 +953,7 @@ __global__ void __launch_bounds__(512, 2) relu2_requant_q8_kernel(const Relu2Par
       const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
       const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
       sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
-      store_unit_bytes(p.Rq + m * p.H, unit_column(g.tid + i * g.T), w0, w1);
+      store_unit_bytes(p.Rq + m * p.H, unit_column(u0 + 32 * i), w0, w1);
     }
   }
   sum = group_reduce(g, sum, redi, [](int a, int b) { return a + b; });
