@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
 
   // Digits of the lane's MMA columns 8n + g. Columns past the tokens repeat
   // another's: what they sum to is never read.
-  uint32_t xaddr[NT];
+  uint32_t xaddr[NT], xother[NT];  // the two pieces of a lane's 32 bytes
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     int xc;
@@ -434,19 +434,33 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
     else
       xc = (8 * n + g) % (3 * toks);
     xaddr[n] = smem_u32(x) + xc * 128 + 16 * ((2 * t) ^ (xc & 1));
+    xother[n] = xaddr[n] ^ 16u;
   }
-  const uint32_t dsum = smem_u32(x) + R.dsum + 8 * t, cf = smem_u32(x) + R.cf + 8 * t;
+  uint32_t sums = smem_u32(x) + R.dsum + 8 * t;
+  constexpr uint32_t CF = V * SUMS * 4;  // from the sums to what they count
   const bool zs = p.zeros != nullptr;
-  const int magic[4] = {0x4B400000, 0x4B400000, 0x4B400000, 0x4B400000};
+  // The bits of 1.5·2^23 in four registers, out of the compiler's sight: it would
+  // set them anew for every group.
+  int magic[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) asm volatile("mov.b32 %0, 0x4B400000;" : "=r"(magic[e]));
 
   uint32_t src = ring, last = ring + (D - 1) * ST;  // the next stage, the one before it
-  int rb = it0 / KB, kb = it0 - rb * KB, slot = 0;
+  int rb = it0 / KB, kb = it0 - rb * KB, slot = 0, at_kb = 0;
   for (int it = it0; it < it1;) {
     const int begin = kb, end = min(KB, kb + (it1 - it));  // this run's part of row block rb
     float acc[NA][4];
 #pragma unroll
     for (int n = 0; n < NA; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-    uint32_t x_off = kb * R.bytes;
+    if (begin != at_kb) {  // the addresses move on with the blocks
+      const uint32_t move = (begin - at_kb) * R.bytes;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        xaddr[n] += move;
+        xother[n] += move;
+      }
+      sums += move;
+    }
     for (; kb < end; ++kb) {
       // D − 1 blocks are under way; the oldest is next. Past the barrier every
       // lane sees it and is done with the stage before it, which is filled anew.
@@ -484,8 +498,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
 #pragma unroll
         for (int j = 0; j < ND; ++j) {
           const int tile = n * ND + j;
-          const uint32_t at = xaddr[tile] + x_off;  // the other piece of the pair is 16 bytes off
-          const uint4 x0 = lds128(at), x1 = lds128(at ^ 16u);
+          const uint4 x0 = lds128(xaddr[tile]), x1 = lds128(xother[tile]);
           const uint32_t b[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
           for (int v = 0; v < V; ++v) {
@@ -498,11 +511,11 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
             }
           }
         }
-        const uint2 cq = lds64(cf + x_off + 32 * n);
+        const uint2 cq = lds64(sums + CF + 32 * n);
         const float c0 = __uint_as_float(cq.x), c1 = __uint_as_float(cq.y);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const uint2 dq = lds64(dsum + x_off + (v * SUMS + 8 * n) * 4);
+          const uint2 dq = lds64(sums + (v * SUMS + 8 * n) * 4);
           const float t0 = __uint_as_float(dq.x), t1 = __uint_as_float(dq.y);
           float y[4];
 #pragma unroll
@@ -518,11 +531,17 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
           acc[n][3] = fmaf(fmaf(z1[v], t1, y[3]), s1[v] * c1, acc[n][3]);
         }
       }
-      x_off += R.bytes;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        xaddr[n] += R.bytes;
+        xother[n] += R.bytes;
+      }
+      sums += R.bytes;
       last = src;
       src = src == ring + (D - 1) * ST ? ring : src + ST;
     }
     it += end - begin;
+    at_kb = end;
     // The share of row block rb: slot 0 for the run's first, 1 for a later one.
     float* mine = part + ((warp * 2 + slot) * 16 + g) * SUMS + 2 * t;
 #pragma unroll
