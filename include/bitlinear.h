@@ -459,7 +459,7 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
  *     s = bf16((hi − lo)/15), z = Clip(Round(−lo/s), 0, 15),
  *     q = Clip(Round(w/s) + z, 0, 15). The quotients are rounded as the exact
  *     ones, ties to even; s is an fp32 quotient rounded to bf16. A group whose
- *     s is 0 holds zeros.
+ *     s is 0 holds zeros. hi − lo has to be finite.
  *   bl_pack_w4    codes found elsewhere: codes [N, K/2] (the lower column in the
  *     low half of a byte), scales [N, ceil(K/group)] bf16, zero points of the
  *     same shape (or both NULL) → the layout above.
@@ -473,8 +473,9 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
  *     group are exact integers, the rest is fp32. An infinity or NaN makes its
  *     token's results NaN. Above 5 tokens one launch makes the fixed-point
  *     activations in the workspace (bl_linear_w4_workspace_bytes() bytes, 0 up
- *     to 5 tokens) and the product reads them. flags: BL_FLAG_PDL as for
- *     bl_linear_ex. */
+ *     to 5 tokens) and the product reads them; calls that may overlap need a
+ *     workspace each. Y must not overlap an input. flags: BL_FLAG_PDL as for
+ *     bl_linear_ex (W4, scales and zeros are the weights). */
 #define BL_W4_MAX_K 262144
 size_t bl_w4_bytes(int64_t N, int64_t K);
 int64_t bl_w4_scale_count(int64_t N, int64_t K, int group);

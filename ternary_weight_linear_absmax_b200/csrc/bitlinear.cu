@@ -884,16 +884,22 @@ bl_status launch_w4_nt(W4Params p, uint8_t* workspace, bool pdl, int dev, int sm
   const int64_t RB = (p.N + 15) / 16, KB = (p.K + 127) / 128;
   const int toks = (int)(p.M < C::kTok ? p.M : C::kTok);
   // The smallest cluster that fits, one CTA per SM. Clusters keep their slab's
-  // sums in shared memory, at most kW4OutCap bytes of them.
+  // sums in shared memory: at most kW4OutCap bytes of them, and what is left.
   int ranks = 1;
   size_t smem = 0;
   int64_t slabs = 0;
   for (; ranks <= kW4MaxCluster; ranks *= 2) {
-    const int64_t kb = (KB + ranks - 1) / ranks, out_rows = (int64_t)(kW4OutCap / (64 * toks));
+    const int64_t kb = (KB + ranks - 1) / ranks;
     if (kb * W4Record<V, NT>(toks).bytes > kW4SmemCap) continue;
+    const size_t fixed = w4_smem<V, NT>((int)kb, 0, toks, ranks).total;
     int64_t n = sms / ranks;
     if (n > RB) n = RB;
-    if (ranks > 1 && n * out_rows < RB) n = (RB + out_rows - 1) / out_rows;
+    if (ranks > 1) {
+      if (fixed + 64 * toks > kW4SmemCap) continue;
+      const size_t room = kW4SmemCap - fixed < kW4OutCap ? kW4SmemCap - fixed : kW4OutCap;
+      const int64_t out_rows = (int64_t)(room / (64 * toks));
+      if (n * out_rows < RB) n = (RB + out_rows - 1) / out_rows;
+    }
     smem = w4_smem<V, NT>((int)kb, (int)((RB + n - 1) / n), toks, ranks).total;
     if (smem > kW4SmemCap) continue;
     slabs = n;

@@ -166,6 +166,100 @@ def test_layernorm_grad_q8(bl, M, K, ddt, odt):
                 dY.double().numpy(), xh, rstd.double().cpu().numpy(), w.astype(np.float64), odt == "bf16", M)
 
 
+# Many rows: the shapes that take other units per thread than a few rows do.
+MANY = [(297, 704), (300, 2560), (310, 4096), (296, 8256), (300, 11008), (298, 16384), (299, 16448)]
+
+
+@pytest.mark.parametrize("M,K", MANY)
+def test_many_rows(bl, M, K):
+    """Rows of a large call against the same rows in small calls (other
+    kernels), bit for bit; gradients against the formulas."""
+    X = _rows(M, K, K, "bf16")
+    w, b = _affine(K, K + 5)
+    Xd, wd, bd = X.to(DEV), _dev(w), _dev(b)
+    big, mean, rstd = bl.bl_layernorm(Xd, wd, bd)
+    tok = bl.bl_layernorm_quant(Xd, wd, bd, checkpoint=True)
+    plain = bl.bl_layernorm_quant(Xd, wd, bd)
+    assert torch.equal(plain[0], tok[0]) and torch.equal(plain[1], tok[1])
+    for r in (0, 1, M // 2, M - 3):
+        part = Xd[r:r + 3].contiguous()
+        y, m3, r3 = bl.bl_layernorm(part, wd, bd)
+        # the order of a row's 64-bit sums is the shape's: far below an fp32 step
+        assert torch.equal(m3, mean[r:r + 3]) and torch.equal(r3, rstd[r:r + 3])
+        assert torch.equal(y, big[r:r + 3])
+        for p, q in zip(bl.bl_layernorm_quant(part, wd, bd, checkpoint=True), tok):
+            assert torch.equal(p, q[r:r + 3])
+    dY = torch.from_numpy(np.random.default_rng(K).standard_normal((M, K)).astype(np.float32))
+    xq, xs = tok[4], tok[5]
+    got = bl.bl_layernorm_grad_q8(dY.to(DEV), xq, xs, rstd, wd)
+    xh = (xq.double() * xs.double().repeat_interleave(64, 1)).cpu().numpy()
+    r = rstd.double().cpu().numpy()
+    _grad_check(*(t.double().cpu().numpy() for t in got), dY.double().numpy(), xh, r, w.astype(np.float64), True, M)
+    got = bl.bl_layernorm_grad(dY.bfloat16().to(DEV), Xd, mean, rstd, wd, out_dtype=torch.float32)
+    xh = (X.double().numpy() - mean.double().cpu().numpy()[:, None]) * r[:, None]
+    _grad_check(*(t.double().cpu().numpy() for t in got), dY.bfloat16().double().numpy(), xh, r,
+                w.astype(np.float64), False, M)
+
+
+@pytest.mark.parametrize("M,H", [(300, 704), (296, 11008)])
+def test_relu2_many_rows(bl, M, H):
+    acc, gx, gu = _acc(M, H, H)
+    a, x, u = _dev(acc), _dev(gx), _dev(gu)
+    big = bl.bl_relu2_requant_q8(a, x, u)
+    none = bl.bl_relu2_requant_q8(a, x, u, checkpoint=False)
+    assert none[3] is None and none[4] is None
+    for p, q in zip(none[:3], big[:3]):
+        assert torch.equal(p, q)
+    for r in (0, 2, M - 2):
+        part = bl.bl_relu2_requant_q8(a[r:r + 2].contiguous(), x[r:r + 2].clone(), u)
+        small = bl.bl_relu2_requant_q8(a[r:r + 2].contiguous(), x[r:r + 2].clone(), u, checkpoint=False)
+        for p, q in zip(part, big):
+            assert torch.equal(p, q[r:r + 2])
+        for p, q in zip(small[:3], big[:3]):
+            assert torch.equal(p, q[r:r + 2])
+
+
+def test_rows_past_two_to_the_31_elements(bl):
+    M, K = 528000, 4096
+    X = torch.empty((M, K), dtype=torch.bfloat16, device=DEV).normal_()
+    w, b = (_dev(t) for t in _affine(K, 8))
+    y, mean, rstd = bl.bl_layernorm(X, w, b)
+    tail = X[-5:].contiguous()
+    assert torch.equal(y[-5:], bl.bl_layernorm(tail, w, b)[0])
+    del y
+    tok = bl.bl_layernorm_quant(X, w, b, checkpoint=True)
+    want = bl.bl_layernorm_quant(tail, w, b, checkpoint=True)
+    for p, q in zip(tok, want):
+        assert torch.equal(p[-5:], q)
+    dX, _, _ = bl.bl_layernorm_grad(X, X, mean, rstd, w)
+    assert torch.equal(dX[-5:], bl.bl_layernorm_grad(tail, tail, mean[-5:].clone(), rstd[-5:].clone(), w)[0])
+
+
+def test_two_calls_at_once(bl):
+    """The same calls on two streams at once, each with its own buffers."""
+    M, K = 256, 2048
+    w, b = (_dev(t) for t in _affine(K, 6))
+    X = [_rows(M, K, s, "bf16").to(DEV) for s in (1, 2)]
+    dY = [torch.randn(M, K, device=DEV) for _ in X]
+
+    def step(x, dy, stream=None):
+        t = bl.bl_layernorm_quant(x, w, b, checkpoint=True, stream=stream)
+        return list(t) + list(bl.bl_layernorm_grad_q8(dy, t[4], t[5], t[3], w, stream=stream))
+
+    want = [step(x, dy) for x, dy in zip(X, dY)]
+    streams = [torch.cuda.Stream() for _ in X]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [None, None]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            got[i] = step(X[i], dY[i], s)
+    torch.cuda.synchronize()
+    for g, v in zip(got, want):
+        for p, q in zip(g, v):
+            assert torch.equal(p, q)
+
+
 def test_layernorm_grad_against_differences(bl):
     """Directional derivatives of Σ dY·LN(x) in 64 bits against the kernels' gradients."""
     M, K = 6, 320

@@ -207,3 +207,69 @@ def test_streams_graph_and_repeat(bl):
     for c in chain:
         h = bl.bl_linear_w4(h, W4, sc, N, zeros=zp)
         assert torch.equal(h, c)
+
+
+def test_many_tokens_share_a_workspace_in_order(bl):
+    """Calls of more than five tokens with one caller-owned workspace, chained
+    with programmatic dependent launch: each overwrites what the one before
+    read, in order."""
+    N = K = 2048
+    X, (W4, sc, zp), w = _problem(bl, 20, N, K, 64, True, "bf16", 12)
+    X = X.to(DEV)
+    L = bl.load()
+    ws = torch.empty(int(L.bl_linear_w4_workspace_bytes(20, K, 64)), dtype=torch.uint8, device=DEV)
+    want, h = [], X
+    for _ in range(6):
+        h = (bl.bl_linear_w4(h, W4, sc, N, zeros=zp) * 0.1).contiguous()
+        want.append(h)
+    h = X
+    for i in range(6):
+        h = (bl.bl_linear_w4(h, W4, sc, N, zeros=zp, workspace=ws, pdl=True) * 0.1).contiguous()
+        assert torch.equal(h, want[i])
+    with pytest.raises(bl.BitLinearError, match="WORKSPACE"):
+        bl.bl_linear_w4(X, W4, sc, N, zeros=zp, workspace=ws[:64])
+
+
+def test_weights_past_two_to_the_32(bl):
+    """5.4e9 weights (2.7 GB of codes): the last rows equal those of a slice."""
+    N, K = 164000, 32768
+    W4 = torch.randint(0, 256, (N // 16, K // 128, 1024), dtype=torch.uint8, device=DEV)
+    sc = torch.rand((N // 16, K // 128, 8, 1, 2), device=DEV).mul_(0.01).bfloat16()
+    X = torch.randn(2, K, device=DEV).bfloat16()
+    y = bl.bl_linear_w4(X, W4, sc, N, out_dtype=torch.float32)
+    tail = bl.bl_linear_w4(X, W4[-4:].contiguous(), sc[-4:].contiguous(), 64, out_dtype=torch.float32)
+    # the runs of a slab, and so the order of a row's fp32 sums, are the shape's
+    assert torch.allclose(y[:, -64:], tail, rtol=0, atol=float(2.0 ** -20 * y.abs().max()))
+    dense = bl.bl_unpack_w4(W4, sc, N, K, out_dtype=torch.bfloat16)
+    assert torch.equal(dense[-16:], bl.bl_unpack_w4(W4[-1:].contiguous(), sc[-1:].contiguous(), 16, K,
+                                                    out_dtype=torch.bfloat16))
+
+
+def test_long_rows_in_clusters(bl):
+    """The longest rows with every group size, and with more row blocks than a
+    cluster keeps sums of."""
+    for M, N, K, group in ((1, 48, 262144, 32), (2, 33, 262144, 64), (3, 20, 131072, 128), (9, 40, 65536, 32),
+                           (1, 9000, 65536, 32)):
+        _check(bl, M, N, K, group, True, "f32", "f32", seed=M + N)
+
+
+def test_nan_and_infinity_reach_their_token_only(bl):
+    X, (W4, sc, zp), w = _problem(bl, 4, 80, 512, 64, True, "f32", 9)
+    base = bl.bl_linear_w4(X.to(DEV), W4, sc, 80, zeros=zp, out_dtype=torch.float32)
+    X[1, 300], X[3, 5] = float("nan"), float("inf")
+    got = bl.bl_linear_w4(X.to(DEV), W4, sc, 80, zeros=zp, out_dtype=torch.float32)
+    assert torch.isnan(got[1]).all() and torch.isnan(got[3]).all()
+    assert torch.equal(got[[0, 2]], base[[0, 2]])
+
+
+def test_wide_range_within_a_block(bl):
+    """Values of very different size in one 128-column block: off by at most half
+    of 2^-22 of the block's largest value per column, and the sums' own error."""
+    X, (W4, sc, zp), w = _problem(bl, 3, 64, 384, 128, True, "f32", 10)
+    x = X.numpy() * np.exp(np.random.default_rng(1).uniform(-12, 6, X.shape)).astype(np.float32)
+    got = bl.bl_linear_w4(torch.from_numpy(x).to(DEV), W4, sc, 64, zeros=zp, out_dtype=torch.float32)
+    want = x.astype(np.float64) @ w.T
+    top = np.abs(x).reshape(3, 3, 128).max(2)
+    cols = np.abs(w).reshape(64, 3, 128).sum(2)
+    tol = ref.linear_bound(x.astype(np.float64), w, 384, False, want) + 2.0 ** -23 * 2 * (top @ cols.T)
+    assert np.all(np.abs(got.double().cpu().numpy() - want) <= tol)
