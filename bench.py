@@ -896,6 +896,34 @@ def profile_case(name: str) -> int:
             bl.bl_ste_grad_input(dY, pk, g, stream=st)
         for _ in range(2):
             bl.bl_ste_grad_weight(dY, Aq, gA, W, g, EPS, stream=st)
+    elif name in ("w4_decode", "w4_batch"):
+        # 4-bit weights: 1 token (2560 -> 6912) over 8 matrices, 16 tokens (4096 -> 11008) over 4
+        M, K, N, n = (1, 2560, 6912, 8) if name == "w4_decode" else (16, 4096, 11008, 4)
+        mats = [bl.bl_quant_weights_w4(si.weights(N, K, seed=i, dtype="bf16").torch(device), 128)
+                for i in range(n)]
+        X = si.activations(M, K, seed=0, dtype="bf16").torch(device)
+        torch.cuda.synchronize()
+        for i in range(2 * n):
+            w, s, _ = mats[i % n]
+            bl.bl_linear_w4(X, w, s, N, pdl=True, stream=st)
+    elif name in ("norm_step", "relu2_step"):
+        # a training step's layer norm (2048 x 4096) or ReLU² (2048 x 11008) with 8-bit checkpoints
+        M, K = (2048, 4096) if name == "norm_step" else (2048, 11008)
+        dY = torch.randn(M, K, device=device)
+        if name == "norm_step":
+            X = si.activations(M, K, seed=0, dtype="bf16").torch(device)
+            w, b = torch.ones(K, device=device), torch.zeros(K, device=device)
+        else:
+            acc = (dY * 1600).round().int()
+            gx, gu = torch.full((M,), 4.0, device=device), torch.full((1,), 0.016, device=device)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            if name == "norm_step":
+                _, _, _, r, xq, xs = bl.bl_layernorm_quant(X, w, b, EPS, checkpoint=True, stream=st)
+                bl.bl_layernorm_grad_q8(dY, xq, xs, r, w, stream=st)
+            else:
+                *_, pq, ps = bl.bl_relu2_requant_q8(acc, gx, gu, EPS, stream=st)
+                bl.bl_relu2_grad_q8(dY, pq, ps, stream=st)
     else:
         raise SystemExit(f"unknown profile case {name}")
     st.synchronize()
@@ -911,7 +939,8 @@ def main(argv=None):
     ap.add_argument("--no-extra", action="store_true", help="skip the secondary workloads")
     ap.add_argument("--cpu-seconds", type=float, default=12.0)
     ap.add_argument("--profile-case", choices=["decode", "decode_radix3", "skinny", "prefill", "ste",
-                                               "ffn1", "ffn64", "ffn512", "small_chain"],
+                                               "ffn1", "ffn64", "ffn512", "small_chain",
+                                               "w4_decode", "w4_batch", "norm_step", "relu2_step"],
                     help="run one small case for an ncu capture and exit")
     ap.add_argument("--traffic-json", metavar="NCU_CSV",
                     help="write the decode GEMV traffic summary read by the bench line "

@@ -468,8 +468,8 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
  *   bl_linear_w4  Y [M, N] = X·Wᵀ from fp32/bf16 activations [M, K], for few
  *     tokens: up to 16 go through the weights at once, more in passes of 16.
  *     K up to BL_W4_MAX_K. Per token and 128 columns the activations are taken
- *     in fixed point, rounded to 2^-23 of the largest of them or less (what
- *     aligning to it in an fp32 sum would lose); products and the sums of a
+ *     in fixed point, off by at most 1.21e-7 of the largest of them (about
+ *     what aligning to it in an fp32 sum loses); products and the sums of a
  *     group are exact integers, the rest is fp32. An infinity or NaN makes its
  *     token's results NaN. Above 5 tokens one launch makes the fixed-point
  *     activations in the workspace (bl_linear_w4_workspace_bytes() bytes, 0 up

@@ -224,17 +224,13 @@ struct NormParams {
   float* xs;            // [M, K/64]
 };
 
-// x̂ and y of a unit from d = x − μ; y may be d.
-__device__ __forceinline__ void norm_affine_unit(const float (&d)[8], float rstd, const float* weight,
-                                                 const float* bias, int64_t c, float (&xhat)[8],
-                                                 float (&y)[8]) {
+// y of a unit from x̂; y may be x̂.
+__device__ __forceinline__ void norm_affine_unit(const float (&xhat)[8], const float* weight,
+                                                 const float* bias, int64_t c, float (&y)[8]) {
   float w[8];
   load_unit(weight, c, w);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    xhat[j] = __fmul_rn(d[j], rstd);
-    y[j] = __fmul_rn(xhat[j], w[j]);
-  }
+  for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(xhat[j], w[j]);
   if (bias != nullptr) {
     load_unit(bias, c, w);
 #pragma unroll
@@ -378,24 +374,24 @@ __global__ void __launch_bounds__(norm_threads(NU)) layernorm_kernel(const NormP
       if (p.mean != nullptr) p.mean[m] = mean;
       if (p.rstd != nullptr) p.rstd[m] = rstd;
     }
-    float xhat[8];
+    // d becomes x̂, zeros past the row.
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = has(i) ? __fmul_rn(v[i][j], rstd) : 0.f;
+    }
     if constexpr (sizeof(OUT) > 1) {
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         if (has(i)) {
           const int64_t c = unit_column(u0 + 32 * i);
-          norm_affine_unit(v[i], rstd, p.weight, p.bias, c, xhat, v[i]);
+          norm_affine_unit(v[i], p.weight, p.bias, c, v[i]);
           store_unit(reinterpret_cast<OUT*>(p.Y) + m * p.K, c, v[i]);
         }
       }
     } else {
       float mx = 0.f;
-      if (p.xq != nullptr) {  // x̂ for the checkpoint first: y takes its place below
-#pragma unroll
-        for (int i = 0; i < NU; ++i) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] = has(i) ? __fmul_rn(v[i][j], rstd) : 0.f;
-        }
+      if (p.xq != nullptr) {
         uint32_t w[NU][2];
         const float sc = ckpt_codes<true, NU>(v, w);
 #pragma unroll
@@ -410,8 +406,7 @@ __global__ void __launch_bounds__(norm_threads(NU)) layernorm_kernel(const NormP
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         if (has(i)) {
-          norm_affine_unit(v[i], p.xq != nullptr ? 1.0f : rstd, p.weight, p.bias,
-                           unit_column(u0 + 32 * i), xhat, v[i]);
+          norm_affine_unit(v[i], p.weight, p.bias, unit_column(u0 + 32 * i), v[i]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[i][j]));
         }
@@ -469,13 +464,13 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
     if (p.mean != nullptr) p.mean[m] = mean;
     if (p.rstd != nullptr) p.rstd[m] = rstd;
   }
-  float xhat[8], y[8];
+  float y[8];
   if constexpr (sizeof(OUT) > 1) {
     for (int64_t u = threadIdx.x; u < units; u += kNormThreads) {
       load_unit(row, unit_column(u), x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = __fsub_rn(x[j], mean);
-      norm_affine_unit(x, rstd, p.weight, p.bias, unit_column(u), xhat, y);
+      for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fsub_rn(x[j], mean), rstd);
+      norm_affine_unit(x, p.weight, p.bias, unit_column(u), y);
       store_unit(reinterpret_cast<OUT*>(p.Y) + m * p.K, unit_column(u), y);
     }
   } else {
@@ -484,18 +479,18 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
     for (int64_t i = 0; i < rounds; ++i) {  // whole warps: a checkpoint group is eight lanes
       const int64_t u = i * kNormThreads + threadIdx.x;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) xhat[j] = 0.f;
+      for (int j = 0; j < 8; ++j) x[j] = 0.f;
       if (u < units) {
         load_unit(row, unit_column(u), x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __fsub_rn(x[j], mean);
-        norm_affine_unit(x, rstd, p.weight, p.bias, unit_column(u), xhat, y);
+        for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fsub_rn(x[j], mean), rstd);
+        norm_affine_unit(x, p.weight, p.bias, unit_column(u), y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(y[j]));
       }
       if (p.xq != nullptr) {
         uint32_t w0, w1;
-        const float sc = ckpt_codes8<true>(xhat, w0, w1);
+        const float sc = ckpt_codes8<true>(x, w0, w1);
         if (u < units) {
           store_unit_bytes(p.xq + m * p.K, unit_column(u), w0, w1);
           if ((u & 7) == 0) p.xs[(m * p.K + 8 * u) / 64] = sc;
@@ -508,8 +503,8 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
     for (int64_t u = threadIdx.x; u < units; u += kNormThreads) {
       load_unit(row, unit_column(u), x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = __fsub_rn(x[j], mean);
-      norm_affine_unit(x, rstd, p.weight, p.bias, unit_column(u), xhat, y);
+      for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fsub_rn(x[j], mean), rstd);
+      norm_affine_unit(x, p.weight, p.bias, unit_column(u), y);
       uint32_t b[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) b[j] = token_bits(y[j], scale);

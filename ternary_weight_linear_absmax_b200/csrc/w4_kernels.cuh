@@ -210,8 +210,8 @@ __device__ __forceinline__ void w4_store(const W4Params& p, int rb, int64_t m0, 
 // together. f is the largest power of two with max|x|·f ≤ 127·2^16; x·f is
 // rounded to a 24-bit integer d2·2^16 + d1·2^8 + d0 with digits in [−128, 127]
 // (adding 0x808080 and flipping the same bits carries between them), and
-// digit i counts 2^(8i)/f. The rounding, half of 1/f, is at most 2^-23 of the
-// block's largest value: what aligning to it in an fp32 sum would lose.
+// digit i counts 2^(8i)/f. The rounding, half of 1/f, is at most 1.21e-7 (2^-22.99)
+// of the block's largest value: about what aligning to it in an fp32 sum loses.
 template <int V, int NT>
 __device__ __forceinline__ void w4_digits(const float (&v)[8], uint8_t* rec, const W4Record<V, NT>& R,
                                           int m, bool write) {

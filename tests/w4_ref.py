@@ -62,13 +62,16 @@ def pack(codes, scales, zps, group, zeros):
 
 
 def linear_bound(x, w, K, bf16_out, ref):
-    """How far fp32 sums may be from the 64-bit product. Products of a bf16
-    piece and a small integer are exact. An MMA adds 16 of them to its
-    accumulator, cutting each of the 17 terms at 2^-24 of the largest at worst;
-    at most 8 MMAs make a group's sum, so a group is off by 8·17·2^-24 of its
-    sum of magnitudes S (three pieces of an fp32 value are added up no worse);
-    the group sums, scaled, meet in chains of K/128/8 fp32 steps per warp and
-    32 more across warps and pieces."""
+    """How far the product may be from the 64-bit one, for values of one scale
+    (normal deviates). Activations are rounded to half of 2^-21.99 of the
+    largest of 128 columns: with a largest value of up to 6.5 times the mean
+    magnitude that is 13·2^-24 of the sum of magnitudes S. A group's products and
+    their sum are exact, and become fp32 with a few operations (8 roundings);
+    the groups' sums are added up in one chain per warp, K/32 at most (its
+    roundings are relative to partial sums, well inside S), and 32 more across
+    warps and digits. The bound below, 136 + K/256 + 36 units of 2^-24, covers
+    these more than once over up to K = 40,000, and what a chain of K/32
+    roundings of random sign adds for longer rows."""
     S = np.abs(x) @ np.abs(w).T
     tol = (8 * 17 + K / 1024 * 4 + 36) * 2.0 ** -24 * S + 1e-37
     return tol + (2.0 ** -8 * np.abs(ref) if bf16_out else 0.0)
