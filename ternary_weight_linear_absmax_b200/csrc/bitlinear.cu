@@ -1039,7 +1039,7 @@ bl_status launch_norm_nu(const NormParams& p, int group, int sms, cudaStream_t s
 // With few rows, a row in the registers of up to 512 threads, as few units each
 // as that allows. With many the looping form, which needs half the registers
 // and reads the row again through L2, keeps more warps busy: 2048 x 11008 takes
-// 35 us in it and 40 with the row kept.
+// 32 us in it and 40 to 45 with the row kept.
 NormShape relu2_shape(int64_t M, int64_t H, int sms) {
   const int64_t units = H / 8;
   for (int nu = 1; nu <= 4 && M < 2 * sms; nu *= 2) {

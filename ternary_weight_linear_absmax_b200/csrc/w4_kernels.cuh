@@ -35,10 +35,10 @@ struct W4Params {
 };
 
 // d = A·B + c.
-__device__ __forceinline__ void mma_u8s8_16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+__device__ __forceinline__ void mma_s8_16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                                uint32_t a3, uint32_t b0, uint32_t b1, const int (&c)[4]) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%10, %11, %12, %13};"
       : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]));
@@ -339,11 +339,14 @@ w4_digits_kernel(const T* __restrict__ X, int64_t M, int64_t K, uint8_t* __restr
 
 // Y = X·Wᵀ for up to W4Pass<NT>::kTok tokens per grid row.
 //
-// Legacy bf16 MMAs run at an eighth of the int8 ones here (m16n8k16 takes 32
-// cycles of a sub-partition's tensor pipe, m16n8k32 of int8 under 9), so the
-// product is one of integers: the codes as bytes against the activations'
-// digits, Σ q·d − z·Σ d exact in int32 for a group, then one fp32
-// multiply-add per group with s times what the digit counts.
+// The product is one of integers: the codes as bytes against the activations'
+// digits, Σ q·d exact in int32 for a group, then in fp32 less z·Σx and times
+// s and what the digit counts. What bounds a decode product here is the
+// issue of instructions, not the tensor pipe (m16n8k16 of bf16 and m16n8k32 of
+// int8 both take 8 cycles of it per sub-partition): as bytes, eight codes take
+// three logic operations and half an MMA, as exact bf16 values (q − z)
+// eleven and one. For 3 x 2048 -> 128256 that was 200 instructions per 1 KB
+// block against 160 now, 37 us against 32.
 //
 // Each CTA owns a slab of 16-row blocks, contiguous in memory; its 16 warps
 // take equal, contiguous runs of the slab's 1 KB blocks, so the load is even
@@ -352,6 +355,14 @@ w4_digits_kernel(const T* __restrict__ X, int64_t M, int64_t K, uint8_t* __restr
 // meet in shared memory at the end, in the order of the warps. The CTAs of a
 // cluster share a slab: each takes a range of K, so that its activations fit
 // in shared memory, and the slab's sums meet there, in the order of the CTAs.
+//
+// Measured (one B200, calls in a graph): 1 x 2560 -> 6912 6.4 us and
+// 4 x 512 -> 256 5.4 us, where a dependent launch, one trip for the activations
+// and one for the weights are what is left; 3 x 2048 -> 128256 32 us, 4.3 TB/s, 67 %
+// of the copy rate, the issue slots 64 % full; 16 x 4096 -> 11008 with zero points
+// and groups of 64 19.4 us with the launch that makes the digits: 24 MMAs and
+// about 370 instructions per 1 KB block, where fp32 work on 16 tokens' sums per
+// group costs more than the weights do.
 template <typename T, int V, int NT>
 __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Params p) {
   using C = W4Pass<NT>;
@@ -505,9 +516,9 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
 #pragma unroll
             for (int u = v * (4 / V); u < (v + 1) * (4 / V); ++u) {
               if (u == v * (4 / V))
-                mma_u8s8_16832(d[j][v], a[u][0], a[u][1], a[u][2], a[u][3], b[2 * u], b[2 * u + 1], magic);
+                mma_s8_16832(d[j][v], a[u][0], a[u][1], a[u][2], a[u][3], b[2 * u], b[2 * u + 1], magic);
               else
-                mma_u8s8_16832(d[j][v], a[u][0], a[u][1], a[u][2], a[u][3], b[2 * u], b[2 * u + 1], d[j][v]);
+                mma_s8_16832(d[j][v], a[u][0], a[u][1], a[u][2], a[u][3], b[2 * u], b[2 * u + 1], d[j][v]);
             }
           }
         }
@@ -667,7 +678,11 @@ __device__ __forceinline__ int64_t w4_group_index(int64_t blk, int r, int v, int
 }
 
 // One CTA per row block (blockIdx.x): sixteen lanes per row, K blocks
-// blockIdx.y, + gridDim.y, ..., two of them under way at a time.
+// blockIdx.y, + gridDim.y, ..., two of them under way at a time. Bound by issue
+// (81 % full at 46 instructions per weight before the group size became a
+// template parameter). With the unpacking kernel after it, 6912 x 2560 bf16 takes
+// 33.8 us (3.7 TB/s, 57 % of the copy rate), 4001 x 4160 fp32 with zero points
+// 35.0 us (4.4 TB/s, 68 %).
 template <typename T, int G, bool ZP>
 __global__ void __launch_bounds__(256)
 w4_quant_kernel(const T* __restrict__ W, int64_t N, int64_t K, uint32_t* __restrict__ W4,
