@@ -520,8 +520,8 @@ def _placed(fn):
     call runs."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        first = args[0] if args else next(iter(kw.values()), None)
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        first = next((t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), None)
+        if first is None or not first.is_cuda:
             return fn(*args, **kw)      # refused there
         if stream is not None:
             if stream.device != first.device:
@@ -535,12 +535,15 @@ def _placed(fn):
     return call
 
 
+_OPTIONAL = frozenset(("bias", "zeros", "out", "workspace"))
+
+
 def _on(**tensors) -> int:
     """Checks that the tensors are contiguous and on one CUDA device; returns
     the handle of that device's current stream."""
     dev = -1
     for name, t in tensors.items():
-        if t is None:
+        if t is None and name in _OPTIONAL:
             continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")

@@ -209,6 +209,23 @@ def test_streams_graph_and_repeat(bl):
         assert torch.equal(h, c)
 
 
+def test_keyword_calls_run_on_their_stream(bl, monkeypatch):
+    """The stream that a call names is the one it runs on, also where its first
+    argument is not a tensor."""
+    W = torch.randn(64, 256, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    seen, on = [], bl._on
+    monkeypatch.setattr(bl, "_on", lambda **t: seen.append(on(**t)) or seen[-1])
+    W4, sc, zp = bl.bl_quant_weights_w4(group=32, zeros=True, W=W, stream=side)
+    Y = bl.bl_linear_w4(zeros=zp, N=64, X=W[:3], W4=W4, scales=sc, stream=side)
+    assert seen == [side.cuda_stream] * 2
+    side.synchronize()
+    a, b, c = bl.bl_quant_weights_w4(W, 32, zeros=True)
+    assert torch.equal(a, W4) and torch.equal(b, sc) and torch.equal(c, zp)
+    assert torch.equal(bl.bl_linear_w4(W[:3], a, b, 64, zeros=c), Y)
+
+
 def test_many_tokens_share_a_workspace_in_order(bl):
     """Calls of more than five tokens with one caller-owned workspace, chained
     with programmatic dependent launch: each overwrites what the one before

@@ -140,3 +140,34 @@ def test_binding_refusals():
         bl._check_w4(W4, sc.float(), None, 16, 64)
     with pytest.raises(TypeError, match="zeros must be"):
         bl._check_w4(W4, sc, sc, 16, 64)
+
+
+def test_binding_refuses_missing_tensors():
+    """None in the place of a tensor that a call cannot do without; those it can
+    do without may be left out."""
+    import ternary_weight_linear_absmax_b200 as bl
+    with pytest.raises(TypeError, match="weight must be a CUDA tensor"):
+        bl._on(weight=None, bias=None)
+    for call in (lambda: bl.bl_quant_weights_w4(None), lambda: bl.bl_layernorm(None, None),
+                 lambda: bl.bl_linear_w4(None, None, None, 16),
+                 lambda: bl.bl_quant_weights_w4(group=128, W=None)):
+        with pytest.raises(TypeError, match="must be a CUDA tensor"):
+            call()
+
+
+def test_binding_places_calls_by_any_tensor():
+    """The device and stream of a call by keyword come from its first tensor,
+    whatever stands before it."""
+    import ternary_weight_linear_absmax_b200 as bl
+
+    class OnGpu(torch.Tensor):
+        is_cuda = True
+        device = torch.device("cuda", 1)
+
+    class Stream:
+        device = torch.device("cuda", 0)
+
+    t = torch.zeros(1).as_subclass(OnGpu)
+    for kw in ({"W": t}, {"group": 32, "W": t}, {"zeros": None, "X": t}):
+        with pytest.raises(ValueError, match="stream is on cuda:0"):
+            bl._placed(lambda **k: None)(stream=Stream(), **kw)
