@@ -512,8 +512,8 @@ bl_status bl_linear_w4(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, co
  *     mean is needed.
  * 8-bit checkpoints: groups of 64 columns with one fp32 scale; m = max|v| of a
  * group, codes Round(v·(127/m)), scale m/127 (unsigned: 255); a group with
- * m < 2^-100 holds zeros. An element is off by at most half a step (plus fp32
- * rounding). Inputs and outputs must not overlap. weight and bias are fp32. */
+ * m < 2^-100 holds zeros, one with a NaN in it reads back as NaN. An element is
+ * off by at most half a step (plus fp32 rounding). Inputs and outputs must not overlap. weight and bias are fp32. */
 bl_status bl_layernorm(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, const float* weight,
                        const float* bias, float eps, void* Y, bl_dtype y_dtype, float* mean,
                        float* rstd, bl_stream_t stream);

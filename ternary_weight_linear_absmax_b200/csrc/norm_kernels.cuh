@@ -144,6 +144,22 @@ __device__ __forceinline__ float block_max_f(float v, float* red) {
   return t;
 }
 
+// Maximum for a checkpoint group. x̂ may be NaN (SIGNED), and so is the maximum
+// then; max(h, 0) never is.
+template <bool SIGNED>
+__device__ __forceinline__ float ckpt_max(float a, float b) {
+  if constexpr (!SIGNED) return fmaxf(a, b);
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+// What a code counts; a NaN in the group is kept in its scale.
+template <bool SIGNED>
+__device__ __forceinline__ float ckpt_scale(float m, bool live) {
+  const float s = live ? __fdiv_rn(m, SIGNED ? 127.0f : 255.0f) : 0.f;
+  return SIGNED && m != m ? m : s;
+}
+
 // Checkpoint codes of eight columns of a group held by eight neighbouring
 // lanes (all 32 lanes of the warp take part; lanes without columns pass
 // zeros). Unsigned codes (top 255) take v ≥ 0. Returns the scale.
@@ -152,9 +168,9 @@ __device__ __forceinline__ float ckpt_codes8(const float (&v)[8], uint32_t& w0, 
   constexpr float top = SIGNED ? 127.0f : 255.0f;
   float m = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+  for (int j = 0; j < 8; ++j) m = ckpt_max<SIGNED>(m, fabsf(v[j]));
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 1; o < 8; o <<= 1) m = ckpt_max<SIGNED>(m, __shfl_xor_sync(0xffffffffu, m, o));
   const bool live = m >= kCkptTiny;
   const float inv = live ? __fdiv_rn(top, m) : 0.f;
   uint32_t b[8];
@@ -163,7 +179,7 @@ __device__ __forceinline__ float ckpt_codes8(const float (&v)[8], uint32_t& w0, 
     b[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), 12582912.0f));
   w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
   w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
-  return live ? __fdiv_rn(m, top) : 0.f;
+  return ckpt_scale<SIGNED>(m, live);
 }
 
 // Checkpoint codes of NU units (at most eight) per thread, eight neighbouring
@@ -179,9 +195,9 @@ __device__ __forceinline__ float ckpt_codes(const float (&v)[NU][8], uint32_t (&
   for (int i = 0; i < NU; ++i) {
     float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[i][j]));
+    for (int j = 0; j < 8; ++j) m = ckpt_max<SIGNED>(m, fabsf(v[i][j]));
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 1; o < 8; o <<= 1) m = ckpt_max<SIGNED>(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (l == i) mine = m;
   }
   const bool live = mine >= kCkptTiny;
@@ -196,13 +212,14 @@ __device__ __forceinline__ float ckpt_codes(const float (&v)[NU][8], uint32_t (&
     w[i][0] = pack4_low_bytes(b[0], b[1], b[2], b[3]);
     w[i][1] = pack4_low_bytes(b[4], b[5], b[6], b[7]);
   }
-  return live ? __fdiv_rn(mine, top) : 0.f;
+  return ckpt_scale<SIGNED>(mine, live);
 }
 
 // quant_i8_bits for values that the scale keeps within the int8 range: with
-// s = 127/(max + eps), |v·s| < 127.5, so nothing is clipped.
+// s = 127/(max + eps), |v·s| < 127.5, so nothing is clipped, and what is left of
+// the clip gives a NaN the same code.
 __device__ __forceinline__ uint32_t token_bits(float v, float s) {
-  return __float_as_uint(__fadd_rn(__fmul_rn(v, s), 12582912.0f));
+  return __float_as_uint(__fadd_rn(fmaxf(__fmul_rn(v, s), -128.0f), 12582912.0f));
 }
 
 // ---------------------------------------------------------------------------
@@ -974,7 +991,7 @@ __global__ void __launch_bounds__(512, 2) relu2_requant_q8_kernel(const Relu2Par
 // Many rows, or rows longer than registers hold: the second pass reads them
 // again, through L2. At 32 registers an SM holds eight such CTAs: 2048 x 11008
 // takes 32 us (4.3 TB/s of its 137 MB, bound by issue, 76 % full) against 40 to 45
-// with the row kept in registers, and 56 us with the gradient after it, 82 % of
+// with the row kept in registers, and 57 us with the gradient after it, 80 % of
 // the copy rate for both.
 template <bool KEEP>
 __global__ void __launch_bounds__(kNormThreads) relu2_requant_q8_long_kernel(const Relu2Params p) {

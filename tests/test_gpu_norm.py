@@ -285,6 +285,57 @@ def test_layernorm_grad_against_differences(bl):
             assert abs(got - (up - down) / (2 * h)) <= 1e-4 * (1 + abs(got))
 
 
+@pytest.mark.parametrize("M,K", [(4, 64), (4, 2560), (300, 4096), (4, 16448)])
+def test_nan_and_infinity(bl, M, K):
+    """Rows with a NaN or an infinity give the tokens that bl_quant_acts makes of
+    them, a checkpoint that says so, and leave the other rows alone."""
+    X = _rows(M, K, M + K, "f32")
+    w, b = _affine(K, K)
+    clean = bl.bl_layernorm_quant(X.to(DEV), _dev(w), _dev(b), checkpoint=True)
+    X[1, K - 1] = float("nan")
+    X[2, 3] = float("inf")
+    X = X.to(DEV)
+    Aq, gA, sums, rstd, xq, xs = bl.bl_layernorm_quant(X, _dev(w), _dev(b), checkpoint=True)
+    Y = bl.bl_layernorm(X, _dev(w), _dev(b), out_dtype=torch.float32)[0]
+    q, g, qs = bl.bl_quant_acts(Y)[:3]
+    assert torch.equal(Aq, q) and torch.equal(gA, g) and torch.equal(sums, qs)
+    rest = [m for m in range(M) if m not in (1, 2)]
+    for got, want in zip((Aq, gA, sums, rstd, xq, xs), clean):
+        assert torch.equal(got[rest], want[rest])
+    assert xs[1:3].isnan().all()
+    dY = torch.ones(M, K, device=DEV)
+    dX, dw, db = bl.bl_layernorm_grad_q8(dY, xq, xs, rstd, _dev(w), out_dtype=torch.float32)
+    assert dX[1:3].isnan().all() and dX[rest].isfinite().all()
+    assert dw.isnan().all() and torch.equal(db, torch.full_like(db, M))
+    # an infinite weight: one column of every row
+    w[5] = np.inf
+    Aq, gA = bl.bl_layernorm_quant(X, _dev(w), _dev(b))[:2]
+    q, g = bl.bl_quant_acts(bl.bl_layernorm(X, _dev(w), _dev(b), out_dtype=torch.float32)[0])[:2]
+    assert torch.equal(Aq, q) and torch.equal(gA, g)
+
+
+@pytest.mark.parametrize("M,H", [(4, 64), (4, 2752), (300, 704), (4, 33024)])
+def test_relu2_nan_and_infinity(bl, M, H):
+    """Scales of a token that are infinite or NaN: what the requantisation of the
+    FFN does with them, by its formulas (a NaN passes no maximum)."""
+    acc, gx, gu = _acc(M, H, M + H)
+    gx[0], gx[2] = np.inf, np.nan
+    Rq, gr, sums, Pq, ps = (t.cpu().numpy() for t in bl.bl_relu2_requant_q8(_dev(acc), _dev(gx), _dev(gu)))
+    with np.errstate(all="ignore"):
+        h = acc.astype(np.float32) * ((gx * gu[0]) / np.float32(127))[:, None]
+        p = np.fmax(h, np.float32(0))
+        r = p * p
+        top = r.max(1)
+        v = np.rint(r * (np.float32(127) / (top + np.float32(1e-5)))[:, None])
+    want = np.where(np.isnan(v), -128, v).astype(np.int64)
+    np.testing.assert_array_equal(gr, top)
+    np.testing.assert_array_equal(Rq, want)
+    np.testing.assert_array_equal(sums, want.sum(1))
+    inf = np.isinf(p[0])
+    assert np.all(Pq[0][inf] == 255) and np.all(np.isinf(ps[0]) == inf.reshape(-1, 64).any(1))
+    assert np.all(Pq[2] == 0) and np.all(ps[2] == 0)
+
+
 def test_layernorm_no_rows(bl):
     K = 128
     w, b = (_dev(t) for t in _affine(K, 1))
