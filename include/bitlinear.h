@@ -470,11 +470,13 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
  *     K up to BL_W4_MAX_K. Per token and 128 columns the activations are taken
  *     in fixed point, off by at most 1.21e-7 of the largest of them (about
  *     what aligning to it in an fp32 sum loses); products and the sums of a
- *     group are exact integers, the rest is fp32. An infinity or NaN makes its
- *     token's results NaN. Above 5 tokens one launch makes the fixed-point
+ *     group are exact integers, the rest is fp32. Above 5 tokens bf16
+ *     activations are taken as they are instead: exact products, fp32 sums. An
+ *     infinity or NaN makes its token's results NaN (infinite or NaN where
+ *     bf16 is taken as it is). Above 5 fp32 tokens one launch makes the fixed-point
  *     activations in the workspace (bl_linear_w4_workspace_bytes() bytes, 0 up
- *     to 5 tokens) and the product reads them; calls that may overlap need a
- *     workspace each. Y must not overlap an input. flags: BL_FLAG_PDL as for
+ *     to 5 tokens; bf16 needs none) and the product reads them; calls that may
+ *     overlap need a workspace each. Y must not overlap an input. flags: BL_FLAG_PDL as for
  *     bl_linear_ex (W4, scales and zeros are the weights). */
 #define BL_W4_MAX_K 262144
 size_t bl_w4_bytes(int64_t N, int64_t K);

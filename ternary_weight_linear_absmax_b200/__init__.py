@@ -655,7 +655,7 @@ def bl_linear_w4(X, W4, scales, N: int, *, zeros=None, out_dtype=torch.bfloat16,
         out = _new(out_dtype, M, N)
     _shape(out, (M, N), "out")
     L = load()
-    if workspace is None and M > 5:
+    if workspace is None and M > 5 and X.dtype == torch.float32:
         workspace = _new(torch.uint8, int(L.bl_linear_w4_workspace_bytes(M, K, group)))
     check(L.bl_linear_w4(X.data_ptr(), _dt(X, "X"), M, K, W4.data_ptr(), scales.data_ptr(),
                          _ptr(zeros), N, group, out.data_ptr(), _dt(out, "out"), _ptr(workspace),

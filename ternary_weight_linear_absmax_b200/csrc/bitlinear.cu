@@ -962,8 +962,13 @@ bl_status launch_w4_v(const W4Params& p, uint8_t* ws, bool pdl, int dev, int sms
     q.Y = reinterpret_cast<uint8_t*>(p.Y) + m * p.N * (p.y_bf16 ? 2 : 4);
     q.M = p.M - m < part ? p.M - m : part;
     bl_status s = BL_ERR_SHAPE;
-    if (q.M > 8) s = launch_w4_nt<T, V, 6>(q, ws, pdl, dev, sms, st);
-    if (q.M > 5 && s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 3>(q, ws, pdl, dev, sms, st);
+    if constexpr (sizeof(T) == 2) {  // as bf16, without digits: the kernel's comment
+      if (q.M > 8) s = launch_w4_nt<T, V, -2>(q, ws, pdl, dev, sms, st);
+      if (q.M > 5 && s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, -1>(q, ws, pdl, dev, sms, st);
+    } else {
+      if (q.M > 8) s = launch_w4_nt<T, V, 6>(q, ws, pdl, dev, sms, st);
+      if (q.M > 5 && s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 3>(q, ws, pdl, dev, sms, st);
+    }
     if (q.M > 2 && s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 2>(q, ws, pdl, dev, sms, st);
     if (s == BL_ERR_SHAPE) s = launch_w4_nt<T, V, 1>(q, ws, pdl, dev, sms, st);
     if (s == BL_ERR_SHAPE && q.M > 1) {  // two long rows do not fit: one by one
@@ -2159,7 +2164,7 @@ bl_status bl_linear_w4(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, co
   BL_TRY(check_ptr(scales));
   if (zeros != nullptr) BL_TRY(check_ptr(zeros));
   BL_TRY(check_ptr(Y));
-  if (const size_t need = bl_linear_w4_workspace_bytes(M, K, group); need != 0) {
+  if (const size_t need = bl_linear_w4_workspace_bytes(M, K, group); need != 0 && x_dtype == BL_F32) {
     if (workspace == nullptr || ws_bytes < need) return BL_ERR_WORKSPACE;
     BL_TRY(check_ptr(workspace));
   }

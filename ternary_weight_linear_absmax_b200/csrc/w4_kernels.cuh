@@ -44,6 +44,16 @@ __device__ __forceinline__ void mma_s8_16832(int (&d)[4], uint32_t a0, uint32_t 
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]));
 }
 
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                               const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+        "f"(c[3]));
+}
+
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -100,15 +110,18 @@ constexpr size_t kW4SmemCap = 226 * 1024;
 constexpr size_t kW4OutCap = 32 * 1024;       // sums of a slab
 constexpr int kW4MaxCluster = 8;
 
-// MMA column tiles of a pass and its tokens. An activation is three 8-bit
-// digits, each in an MMA column of its own. With one or two tiles the columns
-// are packed (token c/3, digit c mod 3); otherwise three tiles take the three
-// digits of eight tokens, so that a lane holds a token's digits itself.
+// MMA column tiles of a pass and its tokens. Integer passes (NT > 0): an
+// activation is three 8-bit digits, each in an MMA column of its own. With one or
+// two tiles the columns are packed (token c/3, digit c mod 3); otherwise three
+// tiles take the three digits of eight tokens, so that a lane holds a token's
+// digits itself. bf16 passes (−NT tiles): a column is a token.
 template <int NT>
 struct W4Pass {
-  static constexpr bool kPlanar = NT >= 3;
-  static constexpr int kTok = kPlanar ? 8 * (NT / 3) : 8 * NT / 3;
-  static constexpr int kSums = kPlanar ? 8 * (NT / 3) : 8 * NT;  // sums per weight row
+  static constexpr bool kFloat = NT < 0, kPlanar = NT >= 3;
+  static constexpr int kTiles = kFloat ? -NT : NT;
+  static constexpr int kTok = kFloat ? -8 * NT : kPlanar ? 8 * (NT / 3) : 8 * NT / 3;
+  static constexpr int kSums = kPlanar ? 8 * (NT / 3) : 8 * kTiles;  // sums per weight row
+  static constexpr int kParts = kFloat || kPlanar ? 1 : 3;           // of them per token
 };
 
 // Shared memory of a CTA, in bytes from its start.
@@ -123,11 +136,14 @@ struct W4Smem {
 // fixed-point sums of the groups (float [group][sum]) and what a digit, or 1 in
 // fixed point, counts (float [sum]). A column's eight 16-byte pieces are
 // swapped in pairs in odd columns, so that two columns (the eight lanes of a
-// 16-byte read) fall on different banks.
+// 16-byte read) fall on different banks. bf16 passes: the activations as they
+// are, 256 bytes a token, its four-piece groups swapped in pairs in odd tokens.
 template <int V, int NT>
 struct W4Record {
   uint32_t dsum, cf, bytes;
   __host__ __device__ __forceinline__ explicit W4Record(int toks) {
+    dsum = cf = bytes = 256 * toks;
+    if (W4Pass<NT>::kFloat) return;
     dsum = 3 * toks * 128;
     cf = dsum + V * W4Pass<NT>::kSums * 4;
     bytes = cf + W4Pass<NT>::kSums * 4;
@@ -138,10 +154,11 @@ __host__ __device__ constexpr int w4_stage_bytes() {
   return 1024 + 48 * V;
 }
 // Ring stages per warp: three where the scales make a stage longer, so that the
-// longest rows fit for every group size.
-template <int V>
+// longest rows fit for every group size, and for 16 bf16 tokens, whose rows of
+// 4096 then fit in one CTA instead of two (16 x 4096 -> 11008: 14.5 us against 16.0).
+template <int V, int NT>
 __host__ __device__ constexpr int w4_stages() {
-  return V == 4 ? 3 : 4;
+  return V == 4 || NT == -2 ? 3 : 4;
 }
 // KB: blocks of K of this CTA, at most; slab: row blocks, at most.
 template <int V, int NT>
@@ -150,7 +167,7 @@ __host__ __device__ inline W4Smem w4_smem(int KB, int slab, int toks, int ranks)
   W4Smem s;
   s.part = 0;
   s.ring = s.part + 2 * kW4Warps * 16 * C::kSums * 4;
-  s.out = s.ring + kW4Warps * w4_stages<V>() * w4_stage_bytes<V>();
+  s.out = s.ring + kW4Warps * w4_stages<V, NT>() * w4_stage_bytes<V>();
   s.x = s.out + (ranks > 1 ? slab * toks * 64 : 0);
   s.total = s.x + KB * W4Record<V, NT>(toks).bytes;
   return s;
@@ -184,7 +201,7 @@ __device__ __forceinline__ int w4_warp_of(int i, int items) {
 template <int NT>
 __device__ __forceinline__ float w4_gather(const float* part, int w_lo, int w_hi, int slot_lo, int r,
                                            int c) {
-  constexpr int SUMS = W4Pass<NT>::kSums, P = W4Pass<NT>::kPlanar ? 1 : 3;
+  constexpr int SUMS = W4Pass<NT>::kSums, P = W4Pass<NT>::kParts;
   float y = 0.f;
 #pragma unroll
   for (int pc = P - 1; pc >= 0; --pc) {
@@ -316,6 +333,22 @@ __device__ __forceinline__ void w4_stage_x(uint8_t* x, const W4Record<V, NT>& R,
   }
 }
 
+// bf16 activations into shared memory as they are, zeros past column K.
+template <int V, int NT>
+__device__ __forceinline__ void w4_copy_x(uint32_t x, const W4Record<V, NT>& R, const __nv_bfloat16* X,
+                                          int64_t K, int kb0, int KB, int toks) {
+  const int units = KB * 16;
+  for (int i = threadIdx.x; i < units * toks; i += kW4Threads) {
+    const int m = i / units, r = i - m * units, c = r & 15;
+    const int64_t k = ((int64_t)kb0 * 16 + r) * 8;
+    const int bytes = k < K ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     x + (r >> 4) * R.bytes + m * 256 + 16 * (c ^ (4 * (m & 1)))),
+                 "l"(X + (bytes ? m * K + k : 0)), "r"(bytes)
+                 : "memory");
+  }
+}
+
 // The records of all tokens and blocks in global memory, [pass][kb][record]:
 // with more than a few tokens, making them again in every CTA would take longer
 // than the product. One warp per two blocks of a token (blockIdx.y and on).
@@ -337,6 +370,14 @@ w4_digits_kernel(const T* __restrict__ X, int64_t M, int64_t K, uint8_t* __restr
   }
 }
 
+// Two codes in the low bits of their halves, as bf16, less 128 + z.
+__device__ __forceinline__ uint32_t w4_centre(uint32_t w, uint32_t z) {
+  const uint32_t q = (w & 0x000F000Fu) | 0x43004300u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&q),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&z));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
 // Y = X·Wᵀ for up to W4Pass<NT>::kTok tokens per grid row.
 //
 // The product is one of integers: the codes as bytes against the activations'
@@ -345,8 +386,11 @@ w4_digits_kernel(const T* __restrict__ X, int64_t M, int64_t K, uint8_t* __restr
 // issue of instructions, not the tensor pipe (m16n8k16 of bf16 and m16n8k32 of
 // int8 both take 8 cycles of it per sub-partition): as bytes, eight codes take
 // three logic operations and half an MMA, as exact bf16 values (q − z)
-// eleven and one. For 3 x 2048 -> 128256 that was 200 instructions per 1 KB
-// block against 160 now, 37 us against 32.
+// eleven and one. For 3 x 2048 -> 128256 that is 39 us against 32, and 6.9 against
+// 6.1 for 1 x 2560 -> 6912. Above five tokens, where the digits take three
+// times the MMAs and a token's sums more fp32 work than the codes, bf16
+// activations go through bf16 MMAs as they are: products are exact, a group's
+// sum is the MMA's fp32 one. 16 x 4096 -> 11008 takes 14.5 us so, 19.4 in digits.
 //
 // Each CTA owns a slab of 16-row blocks, contiguous in memory; its 16 warps
 // take equal, contiguous runs of the slab's 1 KB blocks, so the load is even
@@ -360,18 +404,17 @@ w4_digits_kernel(const T* __restrict__ X, int64_t M, int64_t K, uint8_t* __restr
 // 4 x 512 -> 256 5.4 us, where a dependent launch, one trip for the activations
 // and one for the weights are what is left; 3 x 2048 -> 128256 32 us, 4.3 TB/s, 67 %
 // of the copy rate, the issue slots 64 % full; 16 x 4096 -> 11008 with zero points
-// and groups of 64 19.4 us with the launch that makes the digits: 24 MMAs and
-// about 370 instructions per 1 KB block, where fp32 work on 16 tokens' sums per
-// group costs more than the weights do.
+// and groups of 64 14.5 us from bf16 (19.4 us from fp32 with the launch that makes
+// the digits: 24 MMAs and about 370 instructions per 1 KB block).
 template <typename T, int V, int NT>
 __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Params p) {
   using C = W4Pass<NT>;
   constexpr int SUMS = C::kSums, TOK = C::kTok, ST = w4_stage_bytes<V>();
-  constexpr int NA = SUMS / 8;                  // accumulator tiles
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int NA = SUMS / 8, TILES = C::kTiles;  // accumulator tiles
+  extern __shared__ __align__(128) uint8_t w4_mem[];
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  constexpr int D = w4_stages<V>();
+  constexpr int D = w4_stages<V, NT>();
   const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
   // Blocks are counted in 32 bits: 2^31 of them are 2 TB.
   const int KBt = (int)((p.K + 127) / 128);
@@ -385,8 +428,8 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
   const int toks = (int)min((int64_t)TOK, p.M - m0);
   const W4Smem L = w4_smem<V, NT>((KBt + ranks - 1) / ranks, p.slab_rows + (p.slab_more > 0 ? 1 : 0),
                                   (int)min((int64_t)TOK, p.M), ranks);
-  float* part = reinterpret_cast<float*>(smem + L.part);
-  float* out = reinterpret_cast<float*>(smem + L.out);
+  float* part = reinterpret_cast<float*>(w4_mem + L.part);
+  float* out = reinterpret_cast<float*>(w4_mem + L.out);
 
   pdl_launch_dependents();
   // Requests run ahead of the compute loop: 1024 bytes of codes, two pieces
@@ -399,7 +442,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
   const uint8_t* w_src = p.W4 + 16 * lane;
   const uint8_t* aux_src = is_scale ? reinterpret_cast<const uint8_t*>(p.scales) + 16 * lane
                                     : p.zeros + 16 * (lane - 2 * V);
-  const uint32_t ring = smem_u32(smem) + L.ring + warp * (D * ST);
+  const uint32_t ring = smem_u32(w4_mem) + L.ring + warp * (D * ST);
   int q_kb = it0 % KB, left = it1 - it0;  // every CTA has a block of K: clusters are for long rows
   uint32_t q_blk = (uint32_t)(rb0 + it0 / KB) * KBt + kb0 + q_kb;
   auto request = [&](uint32_t dst) {
@@ -418,10 +461,14 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
 
   const int img = (int)min((int64_t)TOK, p.M);
   const W4Record<V, NT> R(img);
-  uint8_t* x = smem + L.x;
+  uint8_t* x = w4_mem + L.x;
   if constexpr (C::kPlanar) {
     const uint8_t* rec = p.digits + ((int64_t)blockIdx.y * KBt + kb0) * R.bytes;
     for (uint32_t i = 16 * tid; i < KB * R.bytes; i += 16 * kW4Threads) cp_async16(smem_u32(x) + i, rec + i);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if constexpr (C::kFloat) {
+    const auto* X = reinterpret_cast<const __nv_bfloat16*>(p.X) + m0 * p.K;
+    w4_copy_x<V, NT>(smem_u32(x), R, X, p.K, kb0, KB, toks);
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     const T* X = reinterpret_cast<const T*>(p.X) + m0 * p.K;
@@ -436,10 +483,16 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
 
   // Digits of the lane's MMA columns 8n + g. Columns past the tokens repeat
   // another's: what they sum to is never read.
-  uint32_t xaddr[NT], xother[NT];  // the two pieces of a lane's 32 bytes
+  uint32_t xaddr[TILES], xother[TILES];  // the two pieces of a lane's 32 bytes (bf16: even and odd ones)
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
+  for (int n = 0; n < TILES; ++n) {
     int xc;
+    if constexpr (C::kFloat) {
+      xc = (8 * n + g) % toks;
+      xaddr[n] = smem_u32(x) + xc * 256 + 16 * t + 64 * (xc & 1);
+      xother[n] = smem_u32(x) + xc * 256 + 16 * t + 64 - 64 * (xc & 1);
+      continue;
+    }
     if constexpr (C::kPlanar)
       xc = (8 * (n / 3) + g) % toks * 3 + n % 3;
     else
@@ -466,7 +519,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
     if (begin != at_kb) {  // the addresses move on with the blocks
       const uint32_t move = (begin - at_kb) * R.bytes;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < TILES; ++n) {
         xaddr[n] += move;
         xother[n] += move;
       }
@@ -480,15 +533,8 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
       request(last);
       const uint4 wlo = lds128(src + 16 * lane), whi = lds128(src + 16 * lane + 512);
       const uint32_t lo[4] = {wlo.x, wlo.y, wlo.z, wlo.w}, hi[4] = {whi.x, whi.y, whi.z, whi.w};
-      uint32_t a[4][4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        a[u][0] = lo[u] & 0x0F0F0F0Fu;
-        a[u][1] = hi[u] & 0x0F0F0F0Fu;
-        a[u][2] = (lo[u] >> 4) & 0x0F0F0F0Fu;
-        a[u][3] = (hi[u] >> 4) & 0x0F0F0F0Fu;
-      }
       float s0[V], s1[V], z0[V], z1[V];
+      uint32_t zz[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const uint32_t s = lds_u32(src + 1024 + (g * V + v) * 4);
@@ -496,54 +542,97 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
         s1[v] = __uint_as_float(s & 0xFFFF0000u);
         uint32_t z = 0x0808u;
         if (zs) z = lds_u16(src + 1024 + 32 * V + (g * V + v) * 2);
+        zz[v] = z;
         // 2^23 + z has z in its low bits
         z0[v] = 8388608.0f - __uint_as_float(0x4B000000u | (z & 0xFFu));
         z1[v] = 8388608.0f - __uint_as_float(0x4B000000u | (z >> 8));
       }
+      if constexpr (C::kFloat) {
+        // (q − z) as exact bf16: the bits of 128 + q less 128 + z. Two MMAs of 16
+        // columns per word: pairs (0, 1) and (2, 3) of the lane's eight.
+        constexpr float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        float d[NA][4];
 #pragma unroll
-      for (int n = 0; n < NA; ++n) {
-        constexpr int ND = C::kPlanar ? 3 : 1;  // tiles of this accumulator: digits, or one
-        // The sums start at the bits of the float 1.5·2^23: what they end as, read
-        // as a float, less 1.5·2^23 is the sum (|sum| < 2^18).
-        int d[ND][V][4];
+        for (int u = 0; u < 4; ++u) {
+          constexpr int L = 4 / V;  // words of a group
+          const int v = u / L;
+          const uint32_t b0 = __byte_perm(zz[v], 0x43u, 0x4040), b1 = __byte_perm(zz[v], 0x43u, 0x4141);
+          uint32_t a[2][4];
 #pragma unroll
-        for (int j = 0; j < ND; ++j) {
-          const int tile = n * ND + j;
-          const uint4 x0 = lds128(xaddr[tile]), x1 = lds128(xother[tile]);
-          const uint32_t b[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+          for (int q = 0; q < 4; ++q) {
+            a[q >> 1][(q & 1) * 2] = w4_centre(lo[u] >> (4 * q), b0);
+            a[q >> 1][(q & 1) * 2 + 1] = w4_centre(hi[u] >> (4 * q), b1);
+          }
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-#pragma unroll
-            for (int u = v * (4 / V); u < (v + 1) * (4 / V); ++u) {
-              if (u == v * (4 / V))
-                mma_s8_16832(d[j][v], a[u][0], a[u][1], a[u][2], a[u][3], b[2 * u], b[2 * u + 1], magic);
-              else
-                mma_s8_16832(d[j][v], a[u][0], a[u][1], a[u][2], a[u][3], b[2 * u], b[2 * u + 1], d[j][v]);
+          for (int n = 0; n < NA; ++n) {
+            const uint4 b = lds128(((u & 1) ? xother[n] : xaddr[n]) + 128 * (u >> 1));
+            if (u % L == 0)
+              mma_bf16_16816(d[n], a[0], b.x, b.y, zero);
+            else
+              mma_bf16_16816(d[n], a[0], b.x, b.y, d[n]);
+            mma_bf16_16816(d[n], a[1], b.z, b.w, d[n]);
+            if (u % L == L - 1) {
+              acc[n][0] = fmaf(d[n][0], s0[v], acc[n][0]);
+              acc[n][1] = fmaf(d[n][1], s0[v], acc[n][1]);
+              acc[n][2] = fmaf(d[n][2], s1[v], acc[n][2]);
+              acc[n][3] = fmaf(d[n][3], s1[v], acc[n][3]);
             }
           }
         }
-        const uint2 cq = lds64(sums + CF + 32 * n);
-        const float c0 = __uint_as_float(cq.x), c1 = __uint_as_float(cq.y);
+      } else {
+        uint32_t a[4][4];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const uint2 dq = lds64(sums + (v * SUMS + 8 * n) * 4);
-          const float t0 = __uint_as_float(dq.x), t1 = __uint_as_float(dq.y);
-          float y[4];
+        for (int u = 0; u < 4; ++u) {
+          a[u][0] = lo[u] & 0x0F0F0F0Fu;
+          a[u][1] = hi[u] & 0x0F0F0F0Fu;
+          a[u][2] = (lo[u] >> 4) & 0x0F0F0F0Fu;
+          a[u][3] = (hi[u] >> 4) & 0x0F0F0F0Fu;
+        }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[e] = __int_as_float(d[0][v][e]) - 12582912.0f;
+        for (int n = 0; n < NA; ++n) {
+          constexpr int ND = C::kPlanar ? 3 : 1;  // tiles of this accumulator: digits, or one
+          // The sums start at the bits of the float 1.5·2^23: what they end as, read
+          // as a float, less 1.5·2^23 is the sum (|sum| < 2^18).
+          int d[ND][V][4];
 #pragma unroll
-            for (int j = 1; j < ND; ++j) y[e] = fmaf(y[e], 256.0f, __int_as_float(d[j][v][e]) - 12582912.0f);
+          for (int j = 0; j < ND; ++j) {
+            const int tile = n * ND + j;
+            const uint4 x0 = lds128(xaddr[tile]), x1 = lds128(xother[tile]);
+            const uint32_t b[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+#pragma unroll
+              for (int u = v * (4 / V); u < (v + 1) * (4 / V); ++u) {
+                if (u == v * (4 / V))
+                  mma_s8_16832(d[j][v], a[u][0], a[u][1], a[u][2], a[u][3], b[2 * u], b[2 * u + 1], magic);
+                else
+                  mma_s8_16832(d[j][v], a[u][0], a[u][1], a[u][2], a[u][3], b[2 * u], b[2 * u + 1], d[j][v]);
+              }
+            }
           }
-          // less z times the activations' sum, then the scales
-          acc[n][0] = fmaf(fmaf(z0[v], t0, y[0]), s0[v] * c0, acc[n][0]);
-          acc[n][1] = fmaf(fmaf(z0[v], t1, y[1]), s0[v] * c1, acc[n][1]);
-          acc[n][2] = fmaf(fmaf(z1[v], t0, y[2]), s1[v] * c0, acc[n][2]);
-          acc[n][3] = fmaf(fmaf(z1[v], t1, y[3]), s1[v] * c1, acc[n][3]);
+          const uint2 cq = lds64(sums + CF + 32 * n);
+          const float c0 = __uint_as_float(cq.x), c1 = __uint_as_float(cq.y);
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const uint2 dq = lds64(sums + (v * SUMS + 8 * n) * 4);
+            const float t0 = __uint_as_float(dq.x), t1 = __uint_as_float(dq.y);
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[e] = __int_as_float(d[0][v][e]) - 12582912.0f;
+#pragma unroll
+              for (int j = 1; j < ND; ++j) y[e] = fmaf(y[e], 256.0f, __int_as_float(d[j][v][e]) - 12582912.0f);
+            }
+            // less z times the activations' sum, then the scales
+            acc[n][0] = fmaf(fmaf(z0[v], t0, y[0]), s0[v] * c0, acc[n][0]);
+            acc[n][1] = fmaf(fmaf(z0[v], t1, y[1]), s0[v] * c1, acc[n][1]);
+            acc[n][2] = fmaf(fmaf(z1[v], t0, y[2]), s1[v] * c0, acc[n][2]);
+            acc[n][3] = fmaf(fmaf(z1[v], t1, y[3]), s1[v] * c1, acc[n][3]);
+          }
         }
       }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < TILES; ++n) {
         xaddr[n] += R.bytes;
         xother[n] += R.bytes;
       }

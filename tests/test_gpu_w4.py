@@ -231,17 +231,18 @@ def test_many_tokens_share_a_workspace_in_order(bl):
     with programmatic dependent launch: each overwrites what the one before
     read, in order."""
     N = K = 2048
-    X, (W4, sc, zp), w = _problem(bl, 20, N, K, 64, True, "bf16", 12)
+    X, (W4, sc, zp), w = _problem(bl, 20, N, K, 64, True, "f32", 12)
     X = X.to(DEV)
     L = bl.load()
     ws = torch.empty(int(L.bl_linear_w4_workspace_bytes(20, K, 64)), dtype=torch.uint8, device=DEV)
     want, h = [], X
     for _ in range(6):
-        h = (bl.bl_linear_w4(h, W4, sc, N, zeros=zp) * 0.1).contiguous()
+        h = (bl.bl_linear_w4(h, W4, sc, N, zeros=zp, out_dtype=torch.float32) * 0.1).contiguous()
         want.append(h)
     h = X
     for i in range(6):
-        h = (bl.bl_linear_w4(h, W4, sc, N, zeros=zp, workspace=ws, pdl=True) * 0.1).contiguous()
+        h = (bl.bl_linear_w4(h, W4, sc, N, zeros=zp, out_dtype=torch.float32, workspace=ws, pdl=True)
+             * 0.1).contiguous()
         assert torch.equal(h, want[i])
     with pytest.raises(bl.BitLinearError, match="WORKSPACE"):
         bl.bl_linear_w4(X, W4, sc, N, zeros=zp, workspace=ws[:64])
@@ -277,6 +278,42 @@ def test_nan_and_infinity_reach_their_token_only(bl):
     got = bl.bl_linear_w4(X.to(DEV), W4, sc, 80, zeros=zp, out_dtype=torch.float32)
     assert torch.isnan(got[1]).all() and torch.isnan(got[3]).all()
     assert torch.equal(got[[0, 2]], base[[0, 2]])
+
+
+@pytest.mark.parametrize("M,N,K,group", [(6, 33, 64, 32), (8, 200, 704, 64), (13, 100, 4096, 128),
+                                         (16, 70, 8192, 32), (23, 48, 1024, 64)])
+def test_bf16_tokens_exact(bl, M, N, K, group):
+    """Whole numbers and scales that are powers of two: every product and sum is a
+    multiple of the smallest scale and below 2^24 of it, so the result is the exact one."""
+    rng = np.random.default_rng(M)
+    G = -(-K // group)
+    codes, z = rng.integers(0, 16, (N, K)), rng.integers(0, 16, (N, G))
+    s = 2.0 ** rng.integers(-2, 2, (N, G))      # |sum| <= 8192·15·15·8 quarters < 2^24
+    nib = torch.from_numpy((codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8)).to(DEV)
+    W4, sc, zp = bl.bl_pack_w4(nib, torch.from_numpy(s).bfloat16().to(DEV), group,
+                               zeros=torch.from_numpy(z.astype(np.uint8)).to(DEV))
+    x = rng.integers(-15, 16, (M, K))
+    X = torch.from_numpy(x).bfloat16().to(DEV)
+    want = x @ ref.dequant(codes, s, z, group).T
+    np.testing.assert_array_equal(bl.bl_linear_w4(X, W4, sc, N, zeros=zp, out_dtype=torch.float32).cpu().numpy(),
+                                  want)
+
+
+@pytest.mark.parametrize("M", [7, 20])
+def test_bf16_nan_and_infinity_reach_their_token_only(bl, M):
+    X, (W4, sc, zp), w = _problem(bl, M, 80, 576, 64, True, "bf16", 9)
+    base = bl.bl_linear_w4(X.to(DEV), W4, sc, 80, zeros=zp, out_dtype=torch.float32)
+    X[1, 570], X[M - 1, 5] = float("nan"), float("inf")
+    got = bl.bl_linear_w4(X.to(DEV), W4, sc, 80, zeros=zp, out_dtype=torch.float32)
+    assert torch.isnan(got[1]).all() and not got[M - 1].isfinite().any()
+    rest = [m for m in range(M) if m not in (1, M - 1)]
+    assert torch.equal(got[rest], base[rest])
+
+
+def test_bf16_rows_too_long_for_sixteen(bl):
+    """Rows whose 16 or 8 bf16 tokens do not fit in a cluster's shared memory."""
+    for M, N, K, group in ((16, 40, 65536, 32), (9, 33, 131072, 64), (6, 20, 262144, 128)):
+        _check(bl, M, N, K, group, True, "bf16", "f32", seed=M)
 
 
 def test_wide_range_within_a_block(bl):

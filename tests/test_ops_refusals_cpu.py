@@ -56,9 +56,9 @@ def test_w4_refusals(lib, p):
     assert lib.bl_linear_w4_workspace_bytes(5, 64, 32) == 0
     assert lib.bl_linear_w4_workspace_bytes(6, 128, 128) >= 6 * 3 * 128
     assert lib.bl_linear_w4_workspace_bytes(17, 128, 128) >= 2 * 16 * 3 * 128
-    assert f(p, 1, 6, 64, p, p, None, 16, 32, p, 1, None, 0, 0, None) == BAD_WS
-    assert f(p, 1, 6, 64, p, p, None, 16, 32, p, 1, p, 64, 0, None) == BAD_WS
-    assert f(p, 1, 6, 64, p, p, None, 16, 32, p, 1, p + 8, 1 << 20, 0, None) == BAD_ALIGN
+    assert f(p, 0, 6, 64, p, p, None, 16, 32, p, 1, None, 0, 0, None) == BAD_WS
+    assert f(p, 0, 6, 64, p, p, None, 16, 32, p, 1, p, 64, 0, None) == BAD_WS
+    assert f(p, 0, 6, 64, p, p, None, 16, 32, p, 1, p + 8, 1 << 20, 0, None) == BAD_ALIGN
     assert f(p, 1, 1, 64, p, p, None, 16, 96, p, 1, None, 0, 0, None) == BAD_SHAPE
     assert f(p, 1, 1, 96, p, p, None, 16, 32, p, 1, None, 0, 0, None) == BAD_SHAPE
     assert f(p, 1, 1, (1 << 22) + 64, p, p, None, 16, 32, p, 1, None, 0, 0, None) == BAD_SHAPE
