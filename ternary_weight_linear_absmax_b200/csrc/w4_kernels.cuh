@@ -155,7 +155,7 @@ __host__ __device__ constexpr int w4_stage_bytes() {
 }
 // Ring stages per warp: three where the scales make a stage longer, so that the
 // longest rows fit for every group size, and for 16 bf16 tokens, whose rows of
-// 4096 then fit in one CTA instead of two (16 x 4096 -> 11008: 14.5 us against 16.0).
+// 4096 then fit in one CTA instead of two (16 x 4096 -> 11008: 1.5 us of 16 less).
 template <int V, int NT>
 __host__ __device__ constexpr int w4_stages() {
   return V == 4 || NT == -2 ? 3 : 4;
@@ -337,15 +337,23 @@ __device__ __forceinline__ void w4_stage_x(uint8_t* x, const W4Record<V, NT>& R,
 template <int V, int NT>
 __device__ __forceinline__ void w4_copy_x(uint32_t x, const W4Record<V, NT>& R, const __nv_bfloat16* X,
                                           int64_t K, int kb0, int KB, int toks) {
-  const int units = KB * 16;
-  for (int i = threadIdx.x; i < units * toks; i += kW4Threads) {
-    const int m = i / units, r = i - m * units, c = r & 15;
-    const int64_t k = ((int64_t)kb0 * 16 + r) * 8;
+  const int c = threadIdx.x & 15;
+  for (int kb = threadIdx.x >> 4; kb < KB; kb += kW4Threads / 16) {
+    const int64_t k = (int64_t)(kb0 + kb) * 128 + 8 * c;
     const int bytes = k < K ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                     x + (r >> 4) * R.bytes + m * 256 + 16 * (c ^ (4 * (m & 1)))),
-                 "l"(X + (bytes ? m * K + k : 0)), "r"(bytes)
-                 : "memory");
+    const __nv_bfloat16* src = X + (bytes ? k : 0);
+    const uint32_t even = x + kb * R.bytes + 16 * c, odd = x + kb * R.bytes + 16 * (c ^ 4) + 256;
+    auto copy = [&](uint32_t dst) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+      src += K;
+    };
+    int m = 0;
+#pragma unroll 4
+    for (; m + 1 < toks; m += 2) {
+      copy(even + 256 * m);
+      copy(odd + 256 * m);
+    }
+    if (m < toks) copy(even + 256 * m);
   }
 }
 
@@ -390,7 +398,7 @@ __device__ __forceinline__ uint32_t w4_centre(uint32_t w, uint32_t z) {
 // 6.1 for 1 x 2560 -> 6912. Above five tokens, where the digits take three
 // times the MMAs and a token's sums more fp32 work than the codes, bf16
 // activations go through bf16 MMAs as they are: products are exact, a group's
-// sum is the MMA's fp32 one. 16 x 4096 -> 11008 takes 14.5 us so, 19.4 in digits.
+// sum is the MMA's fp32 one. 16 x 4096 -> 11008 takes 13.4 us so, 19.4 in digits.
 //
 // Each CTA owns a slab of 16-row blocks, contiguous in memory; its 16 warps
 // take equal, contiguous runs of the slab's 1 KB blocks, so the load is even
@@ -404,7 +412,7 @@ __device__ __forceinline__ uint32_t w4_centre(uint32_t w, uint32_t z) {
 // 4 x 512 -> 256 5.4 us, where a dependent launch, one trip for the activations
 // and one for the weights are what is left; 3 x 2048 -> 128256 32 us, 4.3 TB/s, 67 %
 // of the copy rate, the issue slots 64 % full; 16 x 4096 -> 11008 with zero points
-// and groups of 64 14.5 us from bf16 (19.4 us from fp32 with the launch that makes
+// and groups of 64 13.4 us from bf16 (19.4 us from fp32 with the launch that makes
 // the digits: 24 MMAs and about 370 instructions per 1 KB block).
 template <typename T, int V, int NT>
 __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Params p) {
