@@ -241,7 +241,7 @@ __device__ __forceinline__ void w4_digits(const float (&v)[8], uint8_t* rec, con
 #pragma unroll
   for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   // f = 2^e, at most 2^125: a block below 1e-31 keeps fewer bits
-  const float f0 = __fdiv_rn(8323072.0f, fmaxf(__uint_as_float(top), 1e-31f));
+  const float f0 = __fdiv_rn(127.0f * 65536.0f, fmaxf(__uint_as_float(top), 1e-31f));
   const uint32_t fb = __float_as_uint(f0) & 0xFF800000u;
   const float f = __uint_as_float(fb);
   // 1/f, its exponent mirrored; an infinity or NaN makes the token's results NaN
