@@ -469,9 +469,12 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
  *     tokens: up to 16 go through the weights at once, more in passes of 16.
  *     K up to BL_W4_MAX_K. Per token and 128 columns the activations are taken
  *     in fixed point, off by at most 1.21e-7 of the largest of them (about
- *     what aligning to it in an fp32 sum loses); products and the sums of a
- *     group are exact integers, the rest is fp32. Above 5 tokens bf16
- *     activations are taken as they are instead: exact products, fp32 sums. An
+ *     what aligning to it in an fp32 sum loses); a group's Σ(q − z)·x is made of
+ *     exact integers (above 5 tokens rounded once or twice to fp32 when they are
+ *     joined), the rest is fp32: one rounding per group, relative to the sums of
+ *     s·(q − z)·x and not of s·z·x, and codes at their zero point give exactly 0.
+ *     Above 5 tokens bf16 activations are taken as they are instead: exact
+ *     products, fp32 sums. An
  *     infinity or NaN makes its token's results NaN (infinite or NaN where
  *     bf16 is taken as it is). Above 5 fp32 tokens one launch makes the fixed-point
  *     activations in the workspace (bl_linear_w4_workspace_bytes() bytes, 0 up

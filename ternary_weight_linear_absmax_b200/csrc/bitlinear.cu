@@ -2140,7 +2140,7 @@ size_t bl_linear_w4_workspace_bytes(int64_t M, int64_t K, int group) {
   const int64_t m = M < w4_part_tokens ? M : w4_part_tokens, KB = (K + 127) / 128;
   auto bytes = [&](int64_t tok) {
     const int64_t img = m < tok ? m : tok;
-    return (size_t)((m + tok - 1) / tok) * KB * (size_t)(img * 384 + (128 / group + 1) * tok * 4);
+    return (size_t)((m + tok - 1) / tok) * KB * (size_t)(img * 384 + (2 * (128 / group) + 1) * tok * 4);
   };
   const size_t a = bytes(16), b = bytes(8);
   return a > b ? a : b;

@@ -133,8 +133,10 @@ struct W4Smem {
   uint32_t total;
 };
 // The activations of 128 columns: the digits' MMA columns, 128 bytes each, the
-// fixed-point sums of the groups (float [group][sum]) and what a digit, or 1 in
-// fixed point, counts (float [sum]). A column's eight 16-byte pieces are
+// sums of the groups (float [group][sum]) and what a digit, or 1 in fixed point,
+// counts (float [sum]). A packed column has its digit's sum, |Σd| ≤ 2^14; three-tile
+// tokens have two arrays, the fixed-point sum in multiples of 2^16 and the rest of
+// it (|.| ≤ 2^15): all exact. A column's eight 16-byte pieces are
 // swapped in pairs in odd columns, so that two columns (the eight lanes of a
 // 16-byte read) fall on different banks. bf16 passes: the activations as they
 // are, 256 bytes a token, its four-piece groups swapped in pairs in odd tokens.
@@ -145,7 +147,7 @@ struct W4Record {
     dsum = cf = bytes = 256 * toks;
     if (W4Pass<NT>::kFloat) return;
     dsum = 3 * toks * 128;
-    cf = dsum + V * W4Pass<NT>::kSums * 4;
+    cf = dsum + (W4Pass<NT>::kPlanar ? 2 : 1) * V * W4Pass<NT>::kSums * 4;
     bytes = cf + W4Pass<NT>::kSums * 4;
   }
 };
@@ -254,26 +256,43 @@ __device__ __forceinline__ void w4_digits(const float (&v)[8], uint8_t* rec, con
     fixed += n;
     w[j] = ((uint32_t)n + 0x808080u) ^ 0x808080u;
   }
+  uint2 digit[3];  // digit d: byte d of the eight words
 #pragma unroll
-  for (int o = 1; o < GL; o <<= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
-  if (!write) return;
-#pragma unroll
-  for (int d = 0; d < 3; ++d) {  // digit d: byte d of the eight words
+  for (int d = 0; d < 3; ++d) {
     const uint32_t sel = d | ((4 + d) << 4);
     const uint32_t a04 = __byte_perm(w[0], w[4], sel), a15 = __byte_perm(w[1], w[5], sel);
     const uint32_t a26 = __byte_perm(w[2], w[6], sel), a37 = __byte_perm(w[3], w[7], sel);
+    digit[d] = make_uint2(__byte_perm(a04, a15, 0x5410), __byte_perm(a26, a37, 0x5410));
+  }
+  // The group's sums: of the numbers (≤ 128·2^23), and of the two upper digits
+  // (≤ 2^14 each) side by side in one word; the lowest digit's is what is left.
+  auto sum8 = [](uint2 d) { return dp4a(d.y, 0x01010101u, dp4a(d.x, 0x01010101u, 0)); };
+  int upper = PL ? 0 : sum8(digit[2]) * 65536 + sum8(digit[1]);
+#pragma unroll
+  for (int o = 1; o < GL; o <<= 1) {
+    fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
+    if (!PL) upper += __shfl_xor_sync(0xffffffffu, upper, o);
+  }
+  if (!write) return;
+#pragma unroll
+  for (int d = 0; d < 3; ++d) {
     const int xc = m * 3 + 2 - d;  // the highest digit first
     // [t][u][8 bytes], t = l mod 4, u = l / 4
     const uint32_t off = (((l & 3) * 2 + (l >> 3)) ^ (xc & 1)) * 16 + ((l >> 2) & 1) * 8;
-    *reinterpret_cast<uint2*>(rec + xc * 128 + off) =
-        make_uint2(__byte_perm(a04, a15, 0x5410), __byte_perm(a26, a37, 0x5410));
+    *reinterpret_cast<uint2*>(rec + xc * 128 + off) = digit[d];
   }
-  // The group's sum (|sum| ≤ 128·2^23) goes with the token, or with its lowest
-  // digit's column, which counts 1.
   if (l % GL == 0) {
     float* s = reinterpret_cast<float*>(rec + R.dsum) + (l / GL) * SUMS + (PL ? m : 3 * m);
-    if (!PL) s[0] = s[1] = 0.f;
-    s[PL ? 0 : 2] = (float)fixed;
+    if constexpr (PL) {
+      const int high = (fixed + 32768) >> 16;
+      s[0] = (float)high;
+      s[V * SUMS] = (float)(fixed - high * 65536);
+    } else {
+      const int s1 = (int16_t)(upper & 0xFFFF), s2 = (upper - s1) >> 16;
+      s[0] = (float)s2;
+      s[1] = (float)s1;
+      s[2] = (float)(fixed - s2 * 65536 - s1 * 256);
+    }
   }
   if (l == 0) {
     float* c = reinterpret_cast<float*>(rec + R.cf) + (PL ? m : 3 * m);
@@ -389,8 +408,8 @@ __device__ __forceinline__ uint32_t w4_centre(uint32_t w, uint32_t z) {
 // Y = X·Wᵀ for up to W4Pass<NT>::kTok tokens per grid row.
 //
 // The product is one of integers: the codes as bytes against the activations'
-// digits, Σ q·d exact in int32 for a group, then in fp32 less z·Σx and times
-// s and what the digit counts. What bounds a decode product here is the
+// digits, Σ q·d − z·Σ d exact for a group and digit, then in fp32 times s and
+// what the digit counts. What bounds a decode product here is the
 // issue of instructions, not the tensor pipe (m16n8k16 of bf16 and m16n8k32 of
 // int8 both take 8 cycles of it per sub-partition): as bytes, eight codes take
 // three logic operations and half an MMA, as exact bf16 values (q − z)
@@ -509,7 +528,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
     xother[n] = xaddr[n] ^ 16u;
   }
   uint32_t sums = smem_u32(x) + R.dsum + 8 * t;
-  constexpr uint32_t CF = V * SUMS * 4;  // from the sums to what they count
+  constexpr uint32_t CF = (C::kPlanar ? 2 : 1) * V * SUMS * 4;  // from the sums to what they count
   const bool zs = p.zeros != nullptr;
   // The bits of 1.5·2^23 in four registers, out of the compiler's sight: it would
   // set them anew for every group.
@@ -623,19 +642,33 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             const uint2 dq = lds64(sums + (v * SUMS + 8 * n) * 4);
-            const float t0 = __uint_as_float(dq.x), t1 = __uint_as_float(dq.y);
+            const float t[4] = {__uint_as_float(dq.x), __uint_as_float(dq.y), __uint_as_float(dq.x),
+                                __uint_as_float(dq.y)};
+            // Less z times the activations' sum, within the group and its digit: an
+            // exact integer below 2^19. What is scaled and added up is then
+            // Σ (q − z)·d, and nothing of the size of z·Σ|x| is ever rounded.
             float y[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[e] = __int_as_float(d[0][v][e]) - 12582912.0f;
+            for (int e = 0; e < 4; ++e)
+              y[e] = fmaf(e < 2 ? z0[v] : z1[v], t[e], __int_as_float(d[0][v][e]) - 12582912.0f);
+            if constexpr (C::kPlanar) {
+              // The highest digit is less z times the sum's multiple of 2^16. The two
+              // others join it, each sum exact below 2^24, and the sum's rest goes
+              // last: off by 2^-24 of the group's result, or by nothing.
+              const uint2 rq = lds64(sums + ((V + v) * SUMS + 8 * n) * 4);
+              const float r[4] = {__uint_as_float(rq.x), __uint_as_float(rq.y), __uint_as_float(rq.x),
+                                  __uint_as_float(rq.y)};
 #pragma unroll
-              for (int j = 1; j < ND; ++j) y[e] = fmaf(y[e], 256.0f, __int_as_float(d[j][v][e]) - 12582912.0f);
+              for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int j = 1; j < ND; ++j) y[e] = fmaf(y[e], 256.0f, __int_as_float(d[j][v][e]) - 12582912.0f);
+                y[e] = fmaf(e < 2 ? z0[v] : z1[v], r[e], y[e]);
+              }
             }
-            // less z times the activations' sum, then the scales
-            acc[n][0] = fmaf(fmaf(z0[v], t0, y[0]), s0[v] * c0, acc[n][0]);
-            acc[n][1] = fmaf(fmaf(z0[v], t1, y[1]), s0[v] * c1, acc[n][1]);
-            acc[n][2] = fmaf(fmaf(z1[v], t0, y[2]), s1[v] * c0, acc[n][2]);
-            acc[n][3] = fmaf(fmaf(z1[v], t1, y[3]), s1[v] * c1, acc[n][3]);
+            acc[n][0] = fmaf(y[0], s0[v] * c0, acc[n][0]);
+            acc[n][1] = fmaf(y[1], s0[v] * c1, acc[n][1]);
+            acc[n][2] = fmaf(y[2], s1[v] * c0, acc[n][2]);
+            acc[n][3] = fmaf(y[3], s1[v] * c1, acc[n][3]);
           }
         }
       }
