@@ -215,11 +215,18 @@ __device__ __forceinline__ float ckpt_codes(const float (&v)[NU][8], uint32_t (&
   return ckpt_scale<SIGNED>(mine, live);
 }
 
-// quant_i8_bits for values that the scale keeps within the int8 range: with
-// s = 127/(max + eps), |v·s| < 127.5, so nothing is clipped, and what is left of
-// the clip gives a NaN the same code.
+// quant_i8_bits for values that the scale keeps within the int8 range: with a
+// finite s = 127/(max + eps), |v·s| < 127.5, so nothing is clipped, and what is
+// left of the clip gives a NaN the same code.
 __device__ __forceinline__ uint32_t token_bits(float v, float s) {
   return __float_as_uint(__fadd_rn(fmaxf(__fmul_rn(v, s), -128.0f), 12582912.0f));
+}
+// s is infinite where max + eps is below 3.8e-37. What quant_i8_bits then makes
+// of v is an end of the range (0·s is a NaN); with a scale of 1 token_bits keeps it.
+__device__ __forceinline__ bool token_scale_overflows(float s) { return s > 3.402823466e38f; }
+__device__ __forceinline__ void token_ends(float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = v[j] > 0.0f ? 127.0f : -128.0f;
 }
 
 // ---------------------------------------------------------------------------
@@ -435,7 +442,12 @@ __global__ void __launch_bounds__(norm_threads(NU)) layernorm_kernel(const NormP
         }
       }
       mx = group_reduce(g, mx, redf, [](float a, float b) { return fmaxf(a, b); });
-      const float scale = __fdiv_rn(127.0f, __fadd_rn(mx, p.q_eps));
+      float scale = __fdiv_rn(127.0f, __fadd_rn(mx, p.q_eps));
+      if (token_scale_overflows(scale)) {
+        scale = 1.0f;
+#pragma unroll
+        for (int i = 0; i < NU; ++i) token_ends(v[i]);
+      }
       int sum = 0;
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
@@ -521,13 +533,16 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_long_kernel(const Norm
       }
     }
     mx = block_max_f(mx, redf);
-    const float scale = __fdiv_rn(127.0f, __fadd_rn(mx, p.q_eps));
+    float scale = __fdiv_rn(127.0f, __fadd_rn(mx, p.q_eps));
+    const bool ends = token_scale_overflows(scale);
+    if (ends) scale = 1.0f;
     int sum = 0;
     for (int64_t u = threadIdx.x; u < units; u += kNormThreads) {
       load_unit(row, unit_column(u), x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fsub_rn(x[j], mean), rstd);
       norm_affine_unit(x, p.weight, p.bias, unit_column(u), y);
+      if (ends) token_ends(y);
       uint32_t b[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) b[j] = token_bits(y[j], scale);
@@ -967,7 +982,12 @@ __global__ void __launch_bounds__(512, 2) relu2_requant_q8_kernel(const Relu2Par
     }
   }
   mx = group_reduce(g, mx, redf, [](float a, float b) { return fmaxf(a, b); });
-  const float s = __fdiv_rn(127.0f, __fadd_rn(mx, p.eps));
+  float s = __fdiv_rn(127.0f, __fadd_rn(mx, p.eps));
+  if (token_scale_overflows(s)) {
+    s = 1.0f;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) token_ends(v[i]);
+  }
   int sum = 0;
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
@@ -994,7 +1014,7 @@ __global__ void __launch_bounds__(512, 2) relu2_requant_q8_kernel(const Relu2Par
 // with the row kept in registers, and 57 us with the gradient after it, 80 % of
 // the copy rate for both.
 template <bool KEEP>
-__global__ void __launch_bounds__(kNormThreads) relu2_requant_q8_long_kernel(const Relu2Params p) {
+__global__ void __launch_bounds__(kNormThreads, 8) relu2_requant_q8_long_kernel(const Relu2Params p) {
   __shared__ float redf[kNormThreads / 32];
   __shared__ int redi[kNormThreads / 32];
   const int64_t m = blockIdx.x, units = p.H / 8;
@@ -1025,13 +1045,18 @@ __global__ void __launch_bounds__(kNormThreads) relu2_requant_q8_long_kernel(con
     for (int j = 0; j < 8; ++j) mx = fmaxf(mx, __fmul_rn(v[j], v[j]));
   }
   mx = block_max_f(mx, redf);
-  const float s = __fdiv_rn(127.0f, __fadd_rn(mx, p.eps));
+  float s = __fdiv_rn(127.0f, __fadd_rn(mx, p.eps));
+  const bool ends = token_scale_overflows(s);
+  if (ends) s = 1.0f;
   int sum = 0;
   for (int64_t u = threadIdx.x; u < units; u += kNormThreads) {
     load_p(u, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
+    if (ends) token_ends(v);
     uint32_t b[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) b[j] = token_bits(__fmul_rn(v[j], v[j]), s);
+    for (int j = 0; j < 8; ++j) b[j] = token_bits(v[j], s);
     const uint32_t w0 = pack4_low_bytes(b[0], b[1], b[2], b[3]);
     const uint32_t w1 = pack4_low_bytes(b[4], b[5], b[6], b[7]);
     sum = dp4a(w1, 0x01010101u, dp4a(w0, 0x01010101u, sum));
