@@ -459,7 +459,8 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
  *     s = bf16((hi − lo)/15), z = Clip(Round(−lo/s), 0, 15),
  *     q = Clip(Round(w/s) + z, 0, 15). The quotients are rounded as the exact
  *     ones, ties to even; s is an fp32 quotient rounded to bf16. A group whose
- *     s is 0 holds zeros. hi − lo has to be finite.
+ *     s is 0 holds zeros. hi − lo has to be finite: a group with a NaN in it reads
+ *     back as NaN, one with an infinity as infinities and NaN.
  *   bl_pack_w4    codes found elsewhere: codes [N, K/2] (the lower column in the
  *     low half of a byte), scales [N, ceil(K/group)] bf16, zero points of the
  *     same shape (or both NULL) → the layout above.

@@ -757,8 +757,9 @@ struct W4Rounder {
   float s, inv, up;
   __device__ __forceinline__ explicit W4Rounder(float scale) {
     // exact, and 1/s stays finite; a scale of 0 makes every value 0
+    // (or NaN: whatever the codes, it reads back as NaN)
     up = scale > 0.f ? (scale < 0x1p-60f ? 0x1p80f : 1.0f) : 0.f;
-    s = scale * up;
+    s = scale > 0.f ? scale * up : 0.f;
     inv = s > 0.f ? __fdividef(1.0f, s) : 0.f;
   }
   __device__ __forceinline__ float operator()(float w) const {
@@ -770,6 +771,18 @@ struct W4Rounder {
     return c > 0 ? moved : k;
   }
 };
+
+// Extremes that a NaN in a group passes on to its scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float m;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
 
 template <typename T>
 __device__ __forceinline__ void w4_load8(const T* p, float (&v)[8]) {
@@ -839,13 +852,13 @@ w4_quant_kernel(const T* __restrict__ W, int64_t N, int64_t K, uint32_t* __restr
       float hi = 0.f, lo = 0.f;  // without zero points: hi of the magnitudes
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        hi = fmaxf(hi, ZP ? v[b][j] : fabsf(v[b][j]));
-        if (ZP) lo = fminf(lo, v[b][j]);
+        hi = max_nan(hi, ZP ? v[b][j] : fabsf(v[b][j]));
+        if (ZP) lo = min_nan(lo, v[b][j]);
       }
 #pragma unroll
       for (int o = 1; o < gl; o <<= 1) {
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        if (ZP) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        if (ZP) lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       }
       const float raw = ZP ? __fdiv_rn(__fsub_rn(hi, lo), 15.0f) : __fdiv_rn(hi, 7.0f);
       const __nv_bfloat16 sb = __float2bfloat16_rn(raw);
