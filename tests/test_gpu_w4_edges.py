@@ -47,3 +47,46 @@ def test_broken_weights_stay_broken(bl, N, K, group, zeros, dt, value):
         assert not y[:, rows].isfinite().any()
         assert torch.equal(y[:, ~rows], bl.bl_linear_w4(X, good[0], good[1], N, zeros=good[2],
                                                         out_dtype=torch.float32).cpu()[:, ~rows])
+
+
+@pytest.mark.parametrize("M,K,group", [(20, 2048, 64), (7, 512, 32), (16, 4096, 128)])
+def test_calls_that_share_a_workspace(bl, M, K, group):
+    """fp32 calls of more than five tokens, issued back to back with programmatic
+    dependent launch and one workspace: nothing runs between them, so a call's
+    digits are written as soon as the call before has read its own. Eagerly, and
+    captured and replayed; every call has activations of its own."""
+    N, calls = K, 8
+    g = torch.Generator().manual_seed(K)
+    W = torch.randn(N, K, generator=g).to(DEV)
+    W4, sc, zp = bl.bl_quant_weights_w4(W, group, zeros=True)
+    X = [torch.randn(M, K, generator=g).to(DEV) for _ in range(calls)]
+    want = [bl.bl_linear_w4(x, W4, sc, N, zeros=zp, out_dtype=torch.float32) for x in X]
+    ws = torch.empty(int(bl.load().bl_linear_w4_workspace_bytes(M, K, group)), dtype=torch.uint8, device=DEV)
+    out = [torch.zeros_like(w) for w in want]
+
+    def run():
+        for x, y in zip(X, out):
+            bl.bl_linear_w4(x, W4, sc, N, zeros=zp, out=y, workspace=ws, pdl=True)
+
+    for _ in range(3):
+        run()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        for y in out:
+            y.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    # a chain: each call reads what the one before wrote
+    sc2 = (sc.float() * 0.02).bfloat16()
+    h, chain = X[0], []
+    for _ in range(calls):
+        h = bl.bl_linear_w4(h, W4, sc2, N, zeros=zp, out_dtype=torch.float32)
+        chain.append(h)
+    h = X[0]
+    for y in out:
+        bl.bl_linear_w4(h, W4, sc2, N, zeros=zp, out=y, workspace=ws, pdl=True)
+        h = y
+    assert all(torch.equal(a, b) for a, b in zip(out, chain)) and chain[-1].isfinite().all()
