@@ -495,8 +495,10 @@ def bl_ste_grad_weight(dY, A_q, gamma_A, W, gamma, eps: float = 1e-5, *, stream=
 
 # The current stream's handle and the current device, without the objects that
 # torch.cuda.current_stream() and current_device() go through (3 us a call), and
-# torch's allocator without its argument parsing (0.8 us against 1.9).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# torch's allocator without its argument parsing (0.8 us against 1.9). Builds of
+# torch that lack these names import the package all the same.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 try:
     from torch._C._dynamo.guards import _empty_strided_cuda
 except ImportError:  # pragma: no cover
