@@ -518,8 +518,8 @@ def _new(dtype, *shape):
 def _placed(fn):
     """Runs ``fn`` on the device of its first tensor and on ``stream`` (default:
     that device's current one). Outputs and workspace are allocated on that
-    stream, so that torch does not hand their memory to another one while the
-    call runs."""
+    stream, and the tensors passed in are recorded on it, so that torch does not
+    hand their memory to another one while the call runs."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         first = next((t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), None)
@@ -529,7 +529,12 @@ def _placed(fn):
             if stream.device != first.device:
                 raise ValueError(f"stream is on {stream.device}, the tensors on {first.device}")
             with torch.cuda.stream(stream):
-                return fn(*args, **kw)
+                try:
+                    return fn(*args, **kw)
+                finally:
+                    for t in (*args, *kw.values()):
+                        if isinstance(t, torch.Tensor) and t.is_cuda:
+                            t.record_stream(stream)
         if first.get_device() != torch._C._cuda_getDevice():
             with torch.cuda.device(first.device):
                 return fn(*args, **kw)

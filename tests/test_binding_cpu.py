@@ -28,3 +28,37 @@ else:
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_inputs_are_kept_for_the_stream_they_are_read_on(monkeypatch):
+    """A call on a stream that is not its inputs' own tells torch so, for every
+    tensor and however it is passed: their memory is not handed out again while
+    the call runs. Without ``stream`` there is nothing to tell."""
+    import contextlib
+
+    import torch
+
+    import ternary_weight_linear_absmax_b200 as bl
+
+    class OnGpu(torch.Tensor):
+        is_cuda = True
+        device = torch.device("cuda", 0)
+
+        def get_device(self):
+            return 0
+
+        def record_stream(self, stream):
+            seen.append((id(self), stream))
+
+    class Stream:
+        device = torch.device("cuda", 0)
+
+    seen, stream = [], Stream()
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    a, b, c = (torch.zeros(1).as_subclass(OnGpu) for _ in range(3))
+    call = bl._placed(lambda *args, **kw: len(args))
+    assert call(a, 3, None, b, stream=stream, out=c, pdl=True) == 4
+    assert set(seen) == {(id(t), stream) for t in (a, b, c)} and len(seen) == 3
+    seen.clear()
+    assert call(a, b, out=c) == 2 and seen == []

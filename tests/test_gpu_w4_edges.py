@@ -90,3 +90,26 @@ def test_calls_that_share_a_workspace(bl, M, K, group):
         bl.bl_linear_w4(h, W4, sc2, N, zeros=zp, out=y, workspace=ws, pdl=True)
         h = y
     assert all(torch.equal(a, b) for a, b in zip(out, chain)) and chain[-1].isfinite().all()
+
+
+def test_memory_of_a_side_streams_inputs_is_kept(bl):
+    """A temporary that a call on a side stream reads may be dropped right after
+    the call: its memory is not handed out before the call has run."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    W4, sc, zp = bl.bl_quant_weights_w4(torch.randn(512, 4096, generator=g, device=DEV), 64, zeros=True)
+    side = torch.cuda.Stream()
+    base = torch.randn(64, 4096, generator=g, device=DEV)
+    want = bl.bl_linear_w4(base, W4, sc, 512, zeros=zp, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    X = base.clone()
+    where, shape = X.data_ptr(), X.shape
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)           # about 10 ms of work ahead of the call
+    y = bl.bl_linear_w4(X, W4, sc, 512, zeros=zp, out_dtype=torch.float32, stream=side)
+    del X
+    fresh = torch.empty(shape, device=DEV)
+    assert fresh.data_ptr() != where
+    fresh.fill_(7.0)
+    side.synchronize()
+    assert torch.equal(y, want)
