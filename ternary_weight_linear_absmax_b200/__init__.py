@@ -69,10 +69,15 @@ def _atleast(t: torch.Tensor, n: int, what: str) -> None:
         raise ValueError(f"{what} must hold at least {n} elements, got {t.numel()}")
 
 
-def _ws(nbytes: int, device) -> torch.Tensor | None:
+def _ws(nbytes: int, device, stream=None) -> torch.Tensor | None:
+    """Workspace of one call. It is dropped when the call returns, while the
+    kernels may still run: recorded on the stream that they run on."""
     if nbytes == 0:
         return None
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
 
 
 def _ptr(t):
@@ -118,7 +123,7 @@ def bl_quant_weights(W: torch.Tensor, eps: float = 1e-5, *, out=None, gamma=None
     _atleast(gamma, 1, "gamma")
     L = load()
     if workspace is None:
-        workspace = _ws(int(L.bl_quant_weights_workspace_bytes(N, K)), W.device)
+        workspace = _ws(int(L.bl_quant_weights_workspace_bytes(N, K)), W.device, stream)
     else:
         _cuda(workspace, "workspace")
     check(L.bl_quant_weights(W.data_ptr(), _dt(W, "W"), N, K, float(eps), out.data_ptr(),
@@ -149,7 +154,7 @@ def bl_zero_gemm(A_q: torch.Tensor, W_packed: torch.Tensor, *, stream=None):
         raise ValueError("W_packed must be [N, K/4]")
     acc = torch.empty((M, N), dtype=torch.int32, device=A_q.device)
     L = load()
-    ws = _ws(int(L.bl_zero_gemm_workspace_bytes(M, K, N)), A_q.device)
+    ws = _ws(int(L.bl_zero_gemm_workspace_bytes(M, K, N)), A_q.device, stream)
     check(L.bl_zero_gemm(A_q.data_ptr(), M, K, W_packed.data_ptr(), N, acc.data_ptr(), _ptr(ws),
                          _nbytes(ws), _stream(stream)), "bl_zero_gemm")
     return acc
@@ -176,7 +181,7 @@ def bl_linear_q(A_q, gamma_A, W_packed, gamma, *, rowsum=None, relu2=False,
     _cuda(out, "out")
     _shape(out, (M, N), "out")
     L = load()
-    ws = None if rowsum is not None else _ws(int(L.bl_linear_q_workspace_bytes(M, K, N)), A_q.device)
+    ws = None if rowsum is not None else _ws(int(L.bl_linear_q_workspace_bytes(M, K, N)), A_q.device, stream)
     check(L.bl_linear_q_ex(A_q.data_ptr(), gamma_A.data_ptr(), _ptr(rowsum), M, K,
                            W_packed.data_ptr(), gamma.data_ptr(), N, int(bool(relu2)),
                            out.data_ptr(), _dt(out, "out"), _ptr(ws), _nbytes(ws),
@@ -200,7 +205,7 @@ def bl_linear(A, W_packed, gamma, eps: float = 1e-5, *, relu2=False, out_dtype=t
     _shape(out, (M, N), "out")
     L = load()
     if workspace is None:
-        workspace = _ws(int(L.bl_linear_workspace_bytes(M, K, N)), A.device)
+        workspace = _ws(int(L.bl_linear_workspace_bytes(M, K, N)), A.device, stream)
     else:
         _cuda(workspace, "workspace")
     check(L.bl_linear_ex(A.data_ptr(), _dt(A, "A"), M, K, W_packed.data_ptr(), gamma.data_ptr(),
@@ -252,7 +257,7 @@ def bl_ffn_relu2(X, W_up, gamma_up, W_down, gamma_down, eps: float = 1e-5, *,
     _shape(out, (M, K), "out")
     L = load()
     if workspace is None:
-        workspace = _ws(int(L.bl_ffn_workspace_bytes(M, K, H)), X.device)
+        workspace = _ws(int(L.bl_ffn_workspace_bytes(M, K, H)), X.device, stream)
     else:
         _cuda(workspace, "workspace")
     check(L.bl_ffn_relu2_ex(X.data_ptr(), _dt(X, "X"), M, K, H, W_up.data_ptr(), gamma_up.data_ptr(),
@@ -290,7 +295,7 @@ def bl_linear_taps(A, W_packed, gamma, eps: float = 1e-5, *, relu2=False,
     _atleast(gamma, 1, "gamma")
     out = torch.empty((M, N), dtype=out_dtype, device=A.device)
     L = load()
-    ws = _ws(int(L.bl_linear_workspace_bytes(M, K, N)), A.device)
+    ws = _ws(int(L.bl_linear_workspace_bytes(M, K, N)), A.device, stream)
     taps, s = _taps(M, K, 0, A.device, False, cta)
     check(L.bl_linear_taps(A.data_ptr(), _dt(A, "A"), M, K, W_packed.data_ptr(), gamma.data_ptr(),
                            N, float(eps), int(bool(relu2)), out.data_ptr(), _dt(out, "out"),
@@ -313,7 +318,7 @@ def bl_ffn_relu2_taps(X, W_up, gamma_up, W_down, gamma_down, eps: float = 1e-5, 
     _shape(W_down, (K, H // 4), "W_down")
     out = torch.empty((M, K), dtype=out_dtype, device=X.device)
     L = load()
-    ws = _ws(int(L.bl_ffn_workspace_bytes(M, K, H)), X.device)
+    ws = _ws(int(L.bl_ffn_workspace_bytes(M, K, H)), X.device, stream)
     taps, s = _taps(M, K, H, X.device, True, cta)
     check(L.bl_ffn_relu2_taps(X.data_ptr(), _dt(X, "X"), M, K, H, W_up.data_ptr(),
                               gamma_up.data_ptr(), W_down.data_ptr(), gamma_down.data_ptr(),
@@ -336,7 +341,7 @@ def bl_ffn_tp_up(X, W_up_r, gamma_up, eps: float = 1e-5, *, stream=None):
     gX = torch.empty((M,), dtype=torch.float32, device=X.device)
     rmax = torch.empty((M,), dtype=torch.float32, device=X.device)
     L = load()
-    ws = _ws(int(L.bl_ffn_tp_up_workspace_bytes(M, K)), X.device)
+    ws = _ws(int(L.bl_ffn_tp_up_workspace_bytes(M, K)), X.device, stream)
     check(L.bl_ffn_tp_up(X.data_ptr(), _dt(X, "X"), M, K, H_r, W_up_r.data_ptr(),
                          gamma_up.data_ptr(), float(eps), acc.data_ptr(), gX.data_ptr(),
                          rmax.data_ptr(), _ptr(ws), _nbytes(ws), _stream(stream)), "bl_ffn_tp_up")
@@ -356,7 +361,7 @@ def bl_ffn_tp_down(acc_up, gamma_x, gamma_up, gamma_r, W_down_r, eps: float = 1e
         raise ValueError("W_down_r must be [K_out, H_r/4]")
     out = torch.empty((M, K_out), dtype=torch.int32, device=acc_up.device)
     L = load()
-    ws = _ws(int(L.bl_ffn_tp_down_workspace_bytes(M, H_r)), acc_up.device)
+    ws = _ws(int(L.bl_ffn_tp_down_workspace_bytes(M, H_r)), acc_up.device, stream)
     check(L.bl_ffn_tp_down(acc_up.data_ptr(), gamma_x.data_ptr(), gamma_up.data_ptr(),
                            gamma_r.data_ptr(), M, H_r, W_down_r.data_ptr(), K_out, float(eps),
                            out.data_ptr(), _ptr(ws), _nbytes(ws), _stream(stream)), "bl_ffn_tp_down")
@@ -462,7 +467,7 @@ def bl_ste_grad_input(dY, W_packed, gamma, *, stream=None):
     K = W_packed.shape[1] * 4
     dA = torch.empty((M, K), dtype=torch.float32, device=dY.device)
     L = load()
-    ws = _ws(int(L.bl_ste_grad_input_workspace_bytes(M, N, K)), dY.device)
+    ws = _ws(int(L.bl_ste_grad_input_workspace_bytes(M, N, K)), dY.device, stream)
     check(L.bl_ste_grad_input(dY.data_ptr(), _dt(dY, "dY"), M, N, W_packed.data_ptr(),
                               gamma.data_ptr(), K, dA.data_ptr(), _ptr(ws), _nbytes(ws),
                               _stream(stream)), "bl_ste_grad_input")
@@ -480,7 +485,7 @@ def bl_ste_grad_weight(dY, A_q, gamma_A, W, gamma, eps: float = 1e-5, *, stream=
         raise ValueError("A_q must be [M, K] and W [N, K]")
     dW = torch.empty((N, K), dtype=torch.float32, device=dY.device)
     L = load()
-    ws = _ws(int(L.bl_ste_grad_weight_workspace_bytes(M, N, K)), dY.device)
+    ws = _ws(int(L.bl_ste_grad_weight_workspace_bytes(M, N, K)), dY.device, stream)
     check(L.bl_ste_grad_weight(dY.data_ptr(), _dt(dY, "dY"), M, N, A_q.data_ptr(),
                                gamma_A.data_ptr(), K, W.data_ptr(), _dt(W, "W"), gamma.data_ptr(),
                                float(eps), dW.data_ptr(), _ptr(ws), _nbytes(ws), _stream(stream)),

@@ -62,3 +62,56 @@ def test_inputs_are_kept_for_the_stream_they_are_read_on(monkeypatch):
     assert set(seen) == {(id(t), stream) for t in (a, b, c)} and len(seen) == 3
     seen.clear()
     assert call(a, b, out=c) == 2 and seen == []
+
+
+def test_workspaces_are_kept_for_the_stream_they_are_used_on(monkeypatch):
+    """A workspace that a call allocates and drops is recorded on the stream that
+    the call names: its memory is not handed out again while the kernels run."""
+    import torch
+
+    import ternary_weight_linear_absmax_b200 as bl
+
+    class OnGpu(torch.Tensor):
+        is_cuda = True
+
+        def record_stream(self, stream):
+            seen.append((self.dtype, self.numel(), stream))
+
+    class Stream:
+        cuda_stream = 77
+
+    class Library:
+        def __getattr__(self, name):
+            if name.endswith("workspace_bytes"):
+                return lambda *a: 4096
+            return lambda *a: calls.append((name, a[-1])) or 0
+
+    seen, calls, stream = [], [], Stream()
+    real = torch.empty
+    monkeypatch.setattr(bl, "load", lambda: Library())
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: real(*a, dtype=k["dtype"]).as_subclass(OnGpu))
+
+    def t(*shape, dtype=torch.float32):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+    M, K, N, i8, u8 = 8, 64, 64, torch.int8, torch.uint8
+    x, w, one = t(M, K), t(N, K // 4, dtype=u8), t(1)
+    a, acc = t(M, K, dtype=i8), t(M, N, dtype=torch.int32)
+    with_workspace = [
+        lambda **k: bl.bl_quant_weights(t(N, K), **k), lambda **k: bl.bl_zero_gemm(a, w, **k),
+        lambda **k: bl.bl_linear_q(a, t(M), w, one, **k), lambda **k: bl.bl_linear(x, w, one, **k),
+        lambda **k: bl.bl_ffn_relu2(x, w, one, w, one, **k), lambda **k: bl.bl_linear_taps(x, w, one, **k),
+        lambda **k: bl.bl_ffn_relu2_taps(x, w, one, w, one, **k), lambda **k: bl.bl_ffn_tp_up(x, w, one, **k),
+        lambda **k: bl.bl_ffn_tp_down(acc, t(M), one, t(M), w, **k),
+        lambda **k: bl.bl_ste_grad_input(x, w, one, **k),
+        lambda **k: bl.bl_ste_grad_weight(x, a, t(M), t(N, K), one, **k)]
+    for call in with_workspace:
+        seen.clear()
+        calls.clear()
+        call(stream=stream)
+        assert [s for _, s in calls] == [77]
+        assert seen == [(u8, 4096, stream)], calls
+    given = t(4096, dtype=u8)                  # a workspace of the caller's is the caller's to keep
+    seen.clear()
+    bl.bl_linear(x, w, one, workspace=given, stream=stream)
+    assert seen == []
