@@ -18,7 +18,9 @@ dhᵀ·Â, da = dh·Ŵ_up, and layer norm's backward of da.
 Decoding (``decode``): the same calls without the checkpoints.
 
 Every arithmetic step runs in the CUDA library; this module sequences the calls
-and adds the residual.
+and adds the residual (in the output's type: the block's output and the sum are
+rounded to it once each). A call runs on its input's device, on that
+device's current stream.
 """
 from __future__ import annotations
 
@@ -26,7 +28,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (bl_layernorm_grad_q8, bl_layernorm_quant, bl_linear_q, bl_relu2_grad_q8,
+from . import (_on, bl_layernorm_grad_q8, bl_layernorm_quant, bl_linear_q, bl_relu2_grad_q8,
                bl_relu2_requant_q8, bl_ste_grad_input, bl_ste_grad_weight, bl_zero_gemm)
 
 
@@ -54,6 +56,11 @@ class PreNormFFN:
     eps: float = 1e-5
 
     def _block(self, X, checkpoint: bool):
+        with torch.cuda.device_of(X):
+            _on(X=X, W_up=self.W_up, W_down=self.W_down, gamma_down=self.gamma_down)
+            return self._run(X, checkpoint)
+
+    def _run(self, X, checkpoint: bool):
         A_q, gamma_a, _, rstd, xq, xs = bl_layernorm_quant(X, self.weight, self.bias, self.eps, self.eps,
                                                            checkpoint=checkpoint)
         acc = bl_zero_gemm(A_q, self.W_up)
@@ -74,10 +81,14 @@ class PreNormFFN:
         """Gradients from dY [M, K] (bf16 or fp32) and the latent weights whose
         clip range masks their gradients."""
         A_q, gamma_a, rstd, xq, xs, R_q, gamma_r, p_q, p_s = saved
-        dW_down = bl_ste_grad_weight(dY, R_q, gamma_r, latent_down, self.gamma_down, self.eps)
-        dR = bl_ste_grad_input(dY, self.W_down, self.gamma_down)
-        dH = bl_relu2_grad_q8(dR, p_q, p_s)
-        dW_up = bl_ste_grad_weight(dH, A_q, gamma_a, latent_up, self.gamma_up, self.eps)
-        dA = bl_ste_grad_input(dH, self.W_up, self.gamma_up)
-        dX, dweight, dbias = bl_layernorm_grad_q8(dA, xq, xs, rstd, self.weight, out_dtype=dY.dtype)
-        return PreNormFFNGrads(dX.add_(dY), dW_up, dW_down, dweight, dbias)
+        with torch.cuda.device_of(dY):
+            _on(dY=dY, A_q=A_q, gamma_a=gamma_a, xhat_q=xq, R_q=R_q, gamma_r=gamma_r, P_q=p_q, W_up=self.W_up,
+                gamma_up=self.gamma_up, W_down=self.W_down, gamma_down=self.gamma_down,
+                latent_up=latent_up, latent_down=latent_down)
+            dW_down = bl_ste_grad_weight(dY, R_q, gamma_r, latent_down, self.gamma_down, self.eps)
+            dR = bl_ste_grad_input(dY, self.W_down, self.gamma_down)
+            dH = bl_relu2_grad_q8(dR, p_q, p_s)
+            dW_up = bl_ste_grad_weight(dH, A_q, gamma_a, latent_up, self.gamma_up, self.eps)
+            dA = bl_ste_grad_input(dH, self.W_up, self.gamma_up)
+            dX, dweight, dbias = bl_layernorm_grad_q8(dA, xq, xs, rstd, self.weight, out_dtype=dY.dtype)
+            return PreNormFFNGrads(dX.add_(dY), dW_up, dW_down, dweight, dbias)

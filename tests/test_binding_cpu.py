@@ -115,3 +115,88 @@ def test_workspaces_are_kept_for_the_stream_they_are_used_on(monkeypatch):
     seen.clear()
     bl.bl_linear(x, w, one, workspace=given, stream=stream)
     assert seen == []
+
+
+def _fake_block(monkeypatch, calls):
+    """A PreNormFFN of stand-in tensors on cuda:1; what it calls is only noted,
+    with the device that is current then."""
+    import torch
+
+    import ternary_weight_linear_absmax_b200 as bl
+    from ternary_weight_linear_absmax_b200 import prenorm_ffn as pf
+
+    class OnGpu(torch.Tensor):
+        is_cuda = True
+        dev = 1
+
+        def get_device(self):
+            return self.dev
+
+    def t(dev=1):
+        x = torch.zeros(2, 2).as_subclass(OnGpu)
+        x.dev = dev
+        return x
+
+    current = [0]
+
+    class DeviceOf:
+        def __init__(self, tensor):
+            self.dev = tensor.get_device()
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.dev
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "device_of", DeviceOf)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(bl, "_raw_stream", lambda dev: 0)
+    outputs = {"bl_layernorm_quant": 6, "bl_relu2_requant_q8": 5, "bl_layernorm_grad_q8": 3}
+    for name in ("bl_layernorm_quant", "bl_zero_gemm", "bl_relu2_requant_q8", "bl_linear_q", "bl_ste_grad_weight",
+                 "bl_ste_grad_input", "bl_relu2_grad_q8", "bl_layernorm_grad_q8"):
+        def fake(*a, name=name, **k):
+            calls.append((name, current[0]))
+            return tuple(t() for _ in range(outputs[name])) if name in outputs else t()
+        monkeypatch.setattr(pf, name, fake)
+    return pf.PreNormFFN(t(), t(), t(), t(), t(), t()), t
+
+
+def test_block_runs_on_its_inputs_device(monkeypatch):
+    """The block on a device that is not the current one: every call is made with
+    the input's device current, and the one before is current again afterwards."""
+    import torch
+    calls = []
+    blk, t = _fake_block(monkeypatch, calls)
+    y, saved = blk.forward(t())
+    blk.decode(t())
+    blk.backward(t(), saved, t(), t())
+    assert len(calls) == 4 + 4 + 6 and {dev for _, dev in calls} == {1}, calls
+    assert torch._C._cuda_getDevice() == 0
+
+
+def test_block_refuses_tensors_of_other_devices(monkeypatch):
+    """A matrix, a scale or latent weights on another device than the input are
+    refused before any kernel gets their address."""
+    import pytest
+    calls = []
+    blk, t = _fake_block(monkeypatch, calls)
+    _, saved = blk.forward(t())
+    for name in ("W_up", "W_down", "gamma_down"):
+        kept = getattr(blk, name)
+        setattr(blk, name, t(0))
+        calls.clear()
+        for run in (lambda: blk.forward(t()), lambda: blk.decode(t()), lambda: blk.backward(t(), saved, t(), t())):
+            with pytest.raises(ValueError, match="expected cuda:1"):
+                run()
+        assert calls == []
+        setattr(blk, name, kept)
+    for latent in ((t(0), t()), (t(), t(0))):
+        calls.clear()
+        with pytest.raises(ValueError, match="expected cuda:1"):
+            blk.backward(t(), saved, *latent)
+        assert calls == []
+    calls.clear()
+    with pytest.raises(ValueError, match="expected cuda:0"):
+        blk.backward(t(0), saved, t(), t())       # not where the forward ran
+    assert calls == []
