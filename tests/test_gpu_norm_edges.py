@@ -45,3 +45,19 @@ def test_relu2_tokens_where_the_scale_overflows(bl, M, H, checkpoint):
         got = bl.bl_relu2_requant_q8(acc, gx, gu, eps, checkpoint=checkpoint)
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_no_rows_through_the_block(bl):
+    """A batch without rows: outputs without rows, gradients of zero."""
+    from ternary_weight_linear_absmax_b200.prenorm_ffn import PreNormFFN
+    K, H = 256, 640
+    lu, ld = torch.randn(H, K, device=DEV), torch.randn(K, H, device=DEV)
+    (pu, gu), (pd, gd) = bl.bl_quant_weights(lu), bl.bl_quant_weights(ld)
+    blk = PreNormFFN(torch.ones(K, device=DEV), None, pu, gu, pd, gd)
+    X = torch.empty(0, K, device=DEV, dtype=torch.bfloat16)
+    y, saved = blk.forward(X)
+    assert y.shape == (0, K) and blk.decode(X).shape == (0, K)
+    g = blk.backward(torch.empty_like(X), saved, lu, ld)
+    assert g.dX.shape == (0, K)
+    for t, shape in ((g.dW_up, (H, K)), (g.dW_down, (K, H)), (g.dweight, (K,)), (g.dbias, (K,))):
+        assert t.shape == shape and torch.all(t == 0)
