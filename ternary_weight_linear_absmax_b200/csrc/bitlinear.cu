@@ -17,6 +17,7 @@
 #include "norm_kernels.cuh"
 #include "quant_kernels.cuh"
 #include "skinny_kernel.cuh"
+#include "smem_limits.h"
 #include "ste_kernels.cuh"
 #include "tc_gemm_kernel.cuh"
 #include "w4_kernels.cuh"
@@ -77,29 +78,22 @@ bl_status current_device(int* dev_out, int* sms_out) {
   return BL_OK;
 }
 
-// Opt a kernel into large dynamic shared memory, once per (kernel, device).
+// Opt a kernel into large dynamic shared memory.
+SmemLimits g_smem;
 template <typename F>
 bl_status ensure_smem(F* kernel, int dev, size_t bytes) {
-  struct Entry {
-    const void* fn;
-    int dev;
-    size_t bytes;
-  };
-  static Entry cache[512];
-  static int n = 0;
   std::lock_guard<std::mutex> lk(g_mu);
-  for (int i = 0; i < n; ++i)
-    if (cache[i].fn == (const void*)kernel && cache[i].dev == dev && cache[i].bytes >= bytes)
-      return BL_OK;
-  BL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
-  // Every SM keeps its whole shared memory: with a smaller L1/shared split,
-  // chosen per kernel, an SM that runs one kind of CTA may lack the room for
-  // the next kernel's CTA in a chain of dependent launches, which then
-  // doubles up on another SM (measured: 1-token FFN blocks 13.7 -> 10.5 us).
-  BL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               (int)cudaSharedmemCarveoutMaxShared));
-  if (n < 512) cache[n++] = Entry{(const void*)kernel, dev, bytes};
-  return BL_OK;
+  const bool ok = g_smem.ensure((const void*)kernel, dev, bytes, [&](size_t limit) {
+    // Every SM keeps its whole shared memory: with a smaller L1/shared split,
+    // chosen per kernel, an SM that runs one kind of CTA may lack the room for
+    // the next kernel's CTA in a chain of dependent launches, which then
+    // doubles up on another SM (measured: 1-token FFN blocks 13.7 -> 10.5 us).
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit) ==
+               cudaSuccess &&
+           cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                (int)cudaSharedmemCarveoutMaxShared) == cudaSuccess;
+  });
+  return ok ? BL_OK : BL_ERR_CUDA;
 }
 
 // --------------------------------------------------------------------------
