@@ -990,10 +990,16 @@ bl_status launch_w4(const W4Params& p, int group, uint8_t* ws, bool pdl, int dev
 
 // --------------------------------------------------------------------------
 // Layer norm and 8-bit checkpoints.
-// Units of eight columns per thread and threads per row. With many rows, four
-// while a row then takes at most 256 threads (what the threads of a row
-// exchange costs more than their columns do), else two, for which an SM holds
-// twice the warps, else four again. With few rows, as few units as fit.
+// Units of eight columns per thread and threads per row. With many or long
+// rows, four while a row then takes at most 256 threads (what the threads of a
+// row exchange costs more than their columns do), else two, for which an SM
+// holds twice the warps, else four again. With few short rows, as few units as fit.
+// Measured on 148 SMs, bf16 to tokens with the checkpoint, few units against
+// many, us: rows of 2560 columns 4.5 / 5.5 at 296 rows, 5.4 / 5.7 at 444, 7.4 / 5.9
+// at 592 (but 8.8 / 10.5 at 888 and 19.2 / 21.6 at 2048: 80 of 96 threads busy); 1024
+// columns 3.8 / 3.9 at 296, 4.0 / 3.9 at 444, 6.7 / 4.4 at 888; 3584 columns 4.4 / 5.1 at
+// 37, 5.3 / 5.6 at 296, 8.5 / 6.0 at 444; 4096 columns 4.6 / 4.4 from 1 row on, 5.7 / 5.0 at
+// 296; 8192 columns 7.2 / 5.0 from 1 row on, 12.7 / 6.5 at 296.
 struct NormShape {
   int nu, group;  // nu 0: the row is too long for registers
 };
@@ -1001,7 +1007,7 @@ NormShape norm_shape(int64_t M, int64_t K, int sms) {
   const int64_t units = K / 8;
   auto group = [&](int nu) { return ((units + nu - 1) / nu + 31) / 32 * 32; };
   int nu = 1;
-  if (M >= 2 * sms)
+  if (M >= 3 * sms || K >= 4096)
     nu = group(4) <= 256 ? 4 : 2;
   while (nu <= 4 && group(nu) > norm_threads(nu)) nu *= 2;
   if (nu > 4) return {0, 0};
@@ -1036,14 +1042,18 @@ bl_status launch_norm_nu(const NormParams& p, int group, int sms, cudaStream_t s
   return BL_OK;
 }
 // With few rows, a row in the registers of up to 512 threads, as few units each
-// as that allows. With many the looping form, which needs half the registers
-// and reads the row again through L2, keeps more warps busy: 2048 x 11008 takes
-// 32 us in it and 40 to 45 with the row kept.
+// as that allows; also with many, where all threads have four units. Otherwise the
+// looping form, which needs half the registers and reads the row again through
+// L2, keeps more warps busy. Measured on 148 SMs with the checkpoint, registers
+// against looping, us: 6912 columns 5.7 / 6.8 at 296 rows, 8.6 / 7.6 at 370, 30.8 / 22.0 at
+// 2048; 11008 columns 7.8 / 9.1, 12.1 / 10.3 and 47 / 33; 2752 columns 3.5 / 3.6, 4.2 / 4.0
+// and 16.0 / 12.1; four whole units, 14336 columns, 7.7 / 10.5, 10.4 / 12.5 and 39 / 43,
+// 12288 columns 7.0 / 9.4, 9.7 / 10.7 and 35.8 / 35.5.
 NormShape relu2_shape(int64_t M, int64_t H, int sms) {
   const int64_t units = H / 8;
-  for (int nu = 1; nu <= 4 && M < 2 * sms; nu *= 2) {
+  for (int nu = 1; nu <= 4; nu *= 2) {
     const int64_t g = ((units + nu - 1) / nu + 31) / 32 * 32;
-    if (g <= 512) return {nu, (int)g};
+    if (g <= 512) return M <= 2 * sms || (nu == 4 && units == 4 * g) ? NormShape{nu, (int)g} : NormShape{0, 0};
   }
   return {0, 0};
 }
