@@ -156,8 +156,12 @@ __host__ __device__ constexpr int w4_stage_bytes() {
   return 1024 + 48 * V;
 }
 // Ring stages per warp: three where the scales make a stage longer, so that the
-// longest rows fit for every group size, and for 16 bf16 tokens, whose rows of
-// 4096 then fit in one CTA instead of two (16 x 4096 -> 11008: 1.5 us of 16 less).
+// longest rows fit for every group size, and for passes of 16 bf16 tokens. Those
+// gain nothing from a fourth at any row length: 9, 16 and 32 tokens, K from 1024 to
+// 11008, N = 4096 and 11008 take 0 to 5 % longer with it where it changes nothing
+// else, and rows of 4096 and 8192 need twice the CTAs (16 tokens, 4096 -> 11008 15.9
+// against 13.2 us, 8192 -> 4096 25.5 against 13.9). One token is where it pays
+// (2048 -> 128256, groups of 64, 28.3 against 29.8 us; groups of 128 26.9 against 27.9).
 template <int V, int NT>
 __host__ __device__ constexpr int w4_stages() {
   return V == 4 || NT == -2 ? 3 : 4;
