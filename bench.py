@@ -906,6 +906,13 @@ def profile_case(name: str) -> int:
         for i in range(2 * n):
             w, s, _ = mats[i % n]
             bl.bl_linear_w4(X, w, s, N, pdl=True, stream=st)
+    elif name == "w4_quant":
+        # 4-bit weights made and read back: 4 matrices of 6912 x 2560 (bf16, symmetric)
+        mats = [si.weights(6912, 2560, seed=i, dtype="bf16").torch(device) for i in range(4)]
+        torch.cuda.synchronize()
+        for i in range(8):
+            w, s, _ = bl.bl_quant_weights_w4(mats[i % 4], 128, stream=st)
+            bl.bl_unpack_w4(w, s, 6912, 2560, stream=st)
     elif name in ("norm_step", "relu2_step"):
         # a training step's layer norm (2048 x 4096) or ReLU² (2048 x 11008) with 8-bit checkpoints
         M, K = (2048, 4096) if name == "norm_step" else (2048, 11008)
@@ -940,7 +947,7 @@ def main(argv=None):
     ap.add_argument("--cpu-seconds", type=float, default=12.0)
     ap.add_argument("--profile-case", choices=["decode", "decode_radix3", "skinny", "prefill", "ste",
                                                "ffn1", "ffn64", "ffn512", "small_chain",
-                                               "w4_decode", "w4_batch", "norm_step", "relu2_step"],
+                                               "w4_decode", "w4_batch", "w4_quant", "norm_step", "relu2_step"],
                     help="run one small case for an ncu capture and exit")
     ap.add_argument("--traffic-json", metavar="NCU_CSV",
                     help="write the decode GEMV traffic summary read by the bench line "
