@@ -470,7 +470,7 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
  *     tokens: up to 16 go through the weights at once, more in passes of 16.
  *     K up to BL_W4_MAX_K. Per token and 128 columns the activations are taken
  *     in fixed point, off by at most 1.21e-7 of the largest of them (about
- *     what aligning to it in an fp32 sum loses); a group's Σ(q − z)·x is made of
+ *     what aligning to it in an fp32 sum loses), or 2^-126; a group's Σ(q − z)·x is made of
  *     exact integers (above 5 tokens rounded once or twice to fp32 when they are
  *     joined), the rest is fp32: one rounding per group, relative to the sums of
  *     s·(q − z)·x and not of s·z·x, and codes at their zero point give exactly 0.
@@ -480,7 +480,10 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
  *     bf16 is taken as it is). Above 5 fp32 tokens one launch makes the fixed-point
  *     activations in the workspace (bl_linear_w4_workspace_bytes() bytes, 0 up
  *     to 5 tokens; bf16 needs none) and the product reads them; calls that may
- *     overlap need a workspace each. Y must not overlap an input. flags: BL_FLAG_PDL as for
+ *     overlap need a workspace each. The order of a result's fp32 sums, and so its
+ *     last bits, depend on M, N, K and the device's SMs, and the type of arithmetic
+ *     on M (up to 5 and above): a token alone and in a batch agree to the errors
+ *     above, not bit for bit. Y must not overlap an input. flags: BL_FLAG_PDL as for
  *     bl_linear_ex (W4, scales and zeros are the weights). */
 #define BL_W4_MAX_K 262144
 size_t bl_w4_bytes(int64_t N, int64_t K);
@@ -545,7 +548,8 @@ bl_status bl_layernorm_grad_q8(const void* dY, bl_dtype dy_dtype, const int8_t* 
  *     as in bl_ffn_relu2, and the unsigned checkpoint of p (P_q [M, H] bytes,
  *     p_scale [M, H/64]; both NULL: not kept).
  *   bl_relu2_grad_q8     dH [M, H] = 2·p̂·dR, p̂ = p_scale·P_q; dR fp32/bf16, dH
- *     fp32/bf16 (bf16 is what bl_ste_grad_weight / _input take without a copy). */
+ *     fp32/bf16 (bf16 is what bl_ste_grad_weight / _input take without a copy).
+ * Inputs and outputs must not overlap. */
 bl_status bl_relu2_requant_q8(const int32_t* acc_up, const float* gamma_x, const float* gamma_up,
                               int64_t M, int64_t H, float eps, int8_t* R_q, float* gamma_r,
                               int32_t* rowsum, uint8_t* P_q, float* p_scale, bl_stream_t stream);

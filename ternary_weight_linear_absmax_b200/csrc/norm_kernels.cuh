@@ -345,7 +345,7 @@ struct RawUnit {
 // FULL: the units are T·NU, every thread has all of its own. OUT: fp32/bf16
 // rows, or int8_t for the tokens.
 //
-// 2048 x 4096 bf16 to bf16 takes 11.4 us (3.0 TB/s, 46 % of the copy rate), bound
+// 2048 x 4096 bf16 to bf16 takes 11.3 us (3.0 TB/s, 46 % of the copy rate), bound
 // by the latency of the 64-bit sums that a row's threads exchange: four units a
 // thread and 128 threads a row beat two units (12.5 us, twice the warps but twice
 // the exchanges), one (18 us) and a warp per row with sixteen (26-35 us, too few
@@ -1010,9 +1010,9 @@ __global__ void __launch_bounds__(512, 2) relu2_requant_q8_kernel(const Relu2Par
 
 // Many rows (relu2_shape), or rows longer than registers hold: the second pass
 // reads them again, through L2. At 32 registers an SM holds eight such CTAs: 2048 x 11008
-// takes 32 us (4.3 TB/s of its 137 MB, bound by issue, 76 % full) against 40 to 45
-// with the row kept in registers, and 57 us with the gradient after it, 80 % of
-// the copy rate for both.
+// takes 33 us (4.2 TB/s of its 137 MB, bound by issue, 76 % full) against 47 with
+// the row kept in registers, and 58 us with the gradient after it, 79 % of the copy
+// rate for both.
 template <bool KEEP>
 __global__ void __launch_bounds__(kNormThreads, 8) relu2_requant_q8_long_kernel(const Relu2Params p) {
   __shared__ float redf[kNormThreads / 32];

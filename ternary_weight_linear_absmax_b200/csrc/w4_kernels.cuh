@@ -417,11 +417,14 @@ __device__ __forceinline__ uint32_t w4_centre(uint32_t w, uint32_t z) {
 // issue of instructions, not the tensor pipe (m16n8k16 of bf16 and m16n8k32 of
 // int8 both take 8 cycles of it per sub-partition): as bytes, eight codes take
 // three logic operations and half an MMA, as exact bf16 values (q − z)
-// eleven and one. For 3 x 2048 -> 128256 that is 39 us against 32, and 6.9 against
-// 6.1 for 1 x 2560 -> 6912. Above five tokens, where the digits take three
+// eleven and one. For 3 x 2048 -> 128256 that is 38.7 us against 31.9, and 6.5 to 6.9
+// against 6.4 for 1 x 2560 -> 6912. Above five tokens, where the digits take three
 // times the MMAs and a token's sums more fp32 work than the codes, bf16
 // activations go through bf16 MMAs as they are: products are exact, a group's
-// sum is the MMA's fp32 one. 16 x 4096 -> 11008 takes 13.4 us so, 19.4 in digits.
+// sum is the MMA's fp32 one. 16 x 4096 -> 11008 takes 13.4 us so, 20.2 in digits.
+// The border at five is the head's; where a CTA has few row blocks making the
+// digits costs more than the codes: 5 x 4096 -> 4096 in groups of 32 takes 12.2 us,
+// 7.4 as bf16, and 2 x 11008 -> 4096 14.1 and 11.3.
 //
 // Each CTA owns a slab of 16-row blocks, contiguous in memory; its 16 warps
 // take equal, contiguous runs of the slab's 1 KB blocks, so the load is even
@@ -432,11 +435,12 @@ __device__ __forceinline__ uint32_t w4_centre(uint32_t w, uint32_t z) {
 // in shared memory, and the slab's sums meet there, in the order of the CTAs.
 //
 // Measured (one B200, calls in a graph): 1 x 2560 -> 6912 6.4 us and
-// 4 x 512 -> 256 5.4 us, where a dependent launch, one trip for the activations
+// 4 x 512 -> 256 5.5 us, where a dependent launch, one trip for the activations
 // and one for the weights are what is left; 3 x 2048 -> 128256 32 us, 4.3 TB/s, 67 %
 // of the copy rate, the issue slots 64 % full; 16 x 4096 -> 11008 with zero points
-// and groups of 64 13.4 us from bf16 (19.4 us from fp32 with the launch that makes
-// the digits: 24 MMAs and about 370 instructions per 1 KB block).
+// and groups of 64 13.4 us from bf16, no unit above 45 %: the one CTA of an SM
+// waits for all its activations before the first MMA (20.2 us from fp32 with the
+// launch that makes the digits, 24 MMAs per 1 KB block).
 template <typename T, int V, int NT>
 __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Params p) {
   using C = W4Pass<NT>;
@@ -826,10 +830,8 @@ __device__ __forceinline__ int64_t w4_group_index(int64_t blk, int r, int v, int
 
 // One CTA per row block (blockIdx.x): sixteen lanes per row, K blocks
 // blockIdx.y, + gridDim.y, ..., two of them under way at a time. Bound by issue
-// (81 % full at 46 instructions per weight before the group size became a
-// template parameter). With the unpacking kernel after it, 6912 x 2560 bf16 takes
-// 33.8 us (3.7 TB/s, 57 % of the copy rate), 4001 x 4160 fp32 with zero points
-// 35.0 us (4.4 TB/s, 68 %).
+// (82 % full): 6912 x 2560 bf16 in groups of 128 takes 19.5 us (2.3 TB/s, 35 % of the
+// copy rate), 4001 x 4160 fp32 with zero points in groups of 32 20.7 us (3.7 TB/s).
 template <typename T, int G, bool ZP>
 __global__ void __launch_bounds__(256)
 w4_quant_kernel(const T* __restrict__ W, int64_t N, int64_t K, uint32_t* __restrict__ W4,
@@ -909,7 +911,8 @@ w4_pack_kernel(const uint32_t* __restrict__ codes, const __nv_bfloat16* __restri
 }
 
 // The matrix the packed weights stand for: fl32(s·(q − z)) (exact: 8 + 5 bits),
-// rounded once more for a bf16 output. CTAs as in the quantiser. `wide`: W is
+// rounded once more for a bf16 output. CTAs as in the quantiser. Bound by HBM:
+// 6912 x 2560 to fp32 takes 15.4 us (5.2 TB/s, 80 % of the copy rate), to bf16 11.8. `wide`: W is
 // 32-byte aligned, and eight fp32 values go out in one store (whole sectors).
 template <int G>
 __global__ void __launch_bounds__(256)
