@@ -100,16 +100,21 @@ def test_memory_of_a_side_streams_inputs_is_kept(bl):
     side = torch.cuda.Stream()
     base = torch.randn(64, 4096, generator=g, device=DEV)
     want = bl.bl_linear_w4(base, W4, sc, 512, zeros=zp, out_dtype=torch.float32)
-    torch.cuda.synchronize()
     X = base.clone()
-    where, shape = X.data_ptr(), X.shape
     side.wait_stream(torch.cuda.current_stream())
+    # twice: the first call leaves its output's and workspace's memory to the second,
+    # which then allocates nothing anew (an allocation waits for the device)
+    for _ in range(2):
+        y = bl.bl_linear_w4(X, W4, sc, 512, zeros=zp, out_dtype=torch.float32, stream=side)
+        side.synchronize()
+    del y
+    where, shape = X.data_ptr(), X.shape
     with torch.cuda.stream(side):
-        torch.cuda._sleep(20_000_000)           # about 10 ms of work ahead of the call
+        torch.cuda._sleep(100_000_000)          # about 50 ms of work ahead of the call
     y = bl.bl_linear_w4(X, W4, sc, 512, zeros=zp, out_dtype=torch.float32, stream=side)
     del X
     fresh = torch.empty(shape, device=DEV)
-    assert fresh.data_ptr() != where
+    assert fresh.data_ptr() != where or side.query()     # handed out again only once the call has run
     fresh.fill_(7.0)
     side.synchronize()
     assert torch.equal(y, want)
