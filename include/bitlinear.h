@@ -474,9 +474,9 @@ bl_status bl_ste_grad_weight(const void* dY, bl_dtype dy_dtype, int64_t M, int64
  *     exact integers (above 5 tokens rounded once or twice to fp32 when they are
  *     joined), the rest is fp32: one rounding per group, relative to the sums of
  *     s·(q − z)·x and not of s·z·x, and codes at their zero point give exactly 0.
- *     Above 5 tokens bf16 activations are taken as they are instead: exact
- *     products, fp32 sums. An
- *     infinity or NaN makes its token's results NaN (infinite or NaN where
+ *     Above 5 tokens bf16 activations are taken as they are instead (but for rows
+ *     of which eight tokens do not fit in a cluster's shared memory): exact
+ *     products, fp32 sums. An infinity or NaN makes its token's results NaN (infinite or NaN where
  *     bf16 is taken as it is). Above 5 fp32 tokens one launch makes the fixed-point
  *     activations in the workspace (bl_linear_w4_workspace_bytes() bytes, 0 up
  *     to 5 tokens; bf16 needs none) and the product reads them; calls that may

@@ -877,27 +877,35 @@ bl_status launch_w4_nt(W4Params p, uint8_t* workspace, bool pdl, int dev, int sm
   using C = W4Pass<NT>;
   const int64_t RB = (p.N + 15) / 16, KB = (p.K + 127) / 128;
   const int toks = (int)(p.M < C::kTok ? p.M : C::kTok);
-  // The smallest cluster that fits, one CTA per SM. Clusters keep their slab's
-  // sums in shared memory: at most kW4OutCap bytes of them, and what is left.
-  int ranks = 1;
+  // The smallest cluster that fits, one CTA per SM, with the deepest ring that
+  // does. Clusters keep their slab's sums in shared memory: at most kW4OutCap
+  // bytes of them, and what is left.
+  constexpr int kDeep = w4_stages<V, NT>(), kLow = C::kPlanar ? 3 : kDeep;
+  int ranks = 1, stages = kDeep;
   size_t smem = 0;
   int64_t slabs = 0;
-  for (; ranks <= kW4MaxCluster; ranks *= 2) {
+  auto fits = [&]() {
     const int64_t kb = (KB + ranks - 1) / ranks;
-    if (kb * W4Record<V, NT>(toks).bytes > kW4SmemCap) continue;
-    const size_t fixed = w4_smem<V, NT>((int)kb, 0, toks, ranks).total;
+    if (kb * W4Record<V, NT>(toks).bytes > kW4SmemCap) return false;
+    const size_t fixed = w4_smem<V, NT>((int)kb, 0, toks, ranks, stages).total;
     int64_t n = sms / ranks;
     if (n > RB) n = RB;
     if (ranks > 1) {
-      if (fixed + 64 * toks > kW4SmemCap) continue;
+      if (fixed + 64 * toks > kW4SmemCap) return false;
       const size_t room = kW4SmemCap - fixed < kW4OutCap ? kW4SmemCap - fixed : kW4OutCap;
       const int64_t out_rows = (int64_t)(room / (64 * toks));
       if (n * out_rows < RB) n = (RB + out_rows - 1) / out_rows;
     }
-    smem = w4_smem<V, NT>((int)kb, (int)((RB + n - 1) / n), toks, ranks).total;
-    if (smem > kW4SmemCap) continue;
+    smem = w4_smem<V, NT>((int)kb, (int)((RB + n - 1) / n), toks, ranks, stages).total;
+    if (smem > kW4SmemCap) return false;
     slabs = n;
-    break;
+    return true;
+  };
+  for (; ranks <= kW4MaxCluster && slabs == 0; ranks *= 2) {
+    stages = kDeep;
+    if (fits()) break;
+    stages = ranks <= 2 ? kLow : kDeep;
+    if (stages != kDeep && fits()) break;
   }
   if (slabs == 0) return BL_ERR_SHAPE;
   if constexpr (C::kPlanar) {
@@ -916,7 +924,7 @@ bl_status launch_w4_nt(W4Params p, uint8_t* workspace, bool pdl, int dev, int sm
     p.digits = workspace;
     pdl = true;  // the product may request its weights while the digits are made
   }
-  auto* k = w4_linear_kernel<T, V, NT>;
+  auto* k = stages == kDeep ? w4_linear_kernel<T, V, NT, kDeep> : w4_linear_kernel<T, V, NT, kLow>;
   BL_TRY(ensure_smem(k, dev, smem));
   p.slab_rows = (int)(RB / slabs);
   p.slab_more = (int)(RB % slabs);

@@ -134,9 +134,9 @@ struct W4Smem {
 };
 // The activations of 128 columns: the digits' MMA columns, 128 bytes each, the
 // sums of the groups (float [group][sum]) and what a digit, or 1 in fixed point,
-// counts (float [sum]). A packed column has its digit's sum, |Σd| ≤ 2^14; three-tile
-// tokens have two arrays, the fixed-point sum in multiples of 2^16 and the rest of
-// it (|.| ≤ 2^15): all exact. A column's eight 16-byte pieces are
+// counts (float [sum]). A packed column has its digit's sum, |Σd| ≤ 2^14; a pair of
+// three-tile tokens has four values, their fixed-point sums in multiples of 2^16 and the
+// rests of those (|.| ≤ 2^15): all exact. A column's eight 16-byte pieces are
 // swapped in pairs in odd columns, so that two columns (the eight lanes of a
 // 16-byte read) fall on different banks. bf16 passes: the activations as they
 // are, 256 bytes a token, its four-piece groups swapped in pairs in odd tokens.
@@ -162,18 +162,22 @@ __host__ __device__ constexpr int w4_stage_bytes() {
 // else, and rows of 4096 and 8192 need twice the CTAs (16 tokens, 4096 -> 11008 15.9
 // against 13.2 us, 8192 -> 4096 25.5 against 13.9). One token is where it pays
 // (2048 -> 128256, groups of 64, 28.3 against 29.8 us; groups of 128 26.9 against 27.9).
+// The launcher takes three for fp32 passes of more than five tokens, too, where
+// those fit in one CTA or a pair and four do not (16 tokens, 2560 -> 6912 in groups of
+// 64 13.9 us in pairs, 10.9 in single CTAs). In clusters of four it does not: their
+// grid runs in two waves (16 tokens, 11008 -> 4096 47 us, 37 in clusters of eight).
 template <int V, int NT>
 __host__ __device__ constexpr int w4_stages() {
   return V == 4 || NT == -2 ? 3 : 4;
 }
 // KB: blocks of K of this CTA, at most; slab: row blocks, at most.
 template <int V, int NT>
-__host__ __device__ inline W4Smem w4_smem(int KB, int slab, int toks, int ranks) {
+__host__ __device__ inline W4Smem w4_smem(int KB, int slab, int toks, int ranks, int stages) {
   using C = W4Pass<NT>;
   W4Smem s;
   s.part = 0;
   s.ring = s.part + 2 * kW4Warps * 16 * C::kSums * 4;
-  s.out = s.ring + kW4Warps * w4_stages<V, NT>() * w4_stage_bytes<V>();
+  s.out = s.ring + kW4Warps * stages * w4_stage_bytes<V>();
   s.x = s.out + (ranks > 1 ? slab * toks * 64 : 0);
   s.total = s.x + KB * W4Record<V, NT>(toks).bytes;
   return s;
@@ -253,50 +257,89 @@ __device__ __forceinline__ void w4_digits(const float (&v)[8], uint8_t* rec, con
   // 1/f, its exponent mirrored; an infinity or NaN makes the token's results NaN
   const float unit = __uint_as_float(top < 0x7F800000u ? 0x7F000000u - fb : 0x7FFFFFFFu);
   int fixed = 0;
+  uint32_t outer = 0, middle = 0;
   uint32_t w[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int n = __float2int_rn(__fmul_rn(v[j], f));
-    fixed += n;
-    w[j] = ((uint32_t)n + 0x808080u) ^ 0x808080u;
+    const uint32_t b = (uint32_t)n + 0x808080u;  // its bytes are the digits + 128
+    if (PL) fixed += n;
+    if (NT == 1) {
+      outer += b & 0x00FF00FFu;
+      middle += (b >> 8) & 0xFFu;
+    }
+    w[j] = b ^ 0x808080u;
   }
-  uint2 digit[3];  // digit d: byte d of the eight words
-#pragma unroll
-  for (int d = 0; d < 3; ++d) {
+  auto digit = [&](int d) {  // byte d of the eight words
     const uint32_t sel = d | ((4 + d) << 4);
     const uint32_t a04 = __byte_perm(w[0], w[4], sel), a15 = __byte_perm(w[1], w[5], sel);
     const uint32_t a26 = __byte_perm(w[2], w[6], sel), a37 = __byte_perm(w[3], w[7], sel);
-    digit[d] = make_uint2(__byte_perm(a04, a15, 0x5410), __byte_perm(a26, a37, 0x5410));
-  }
-  // The group's sums: of the numbers (≤ 128·2^23), and of the two upper digits
-  // (≤ 2^14 each) side by side in one word; the lowest digit's is what is left.
-  auto sum8 = [](uint2 d) { return dp4a(d.y, 0x01010101u, dp4a(d.x, 0x01010101u, 0)); };
-  int upper = PL ? 0 : sum8(digit[2]) * 65536 + sum8(digit[1]);
-#pragma unroll
-  for (int o = 1; o < GL; o <<= 1) {
-    fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
-    if (!PL) upper += __shfl_xor_sync(0xffffffffu, upper, o);
-  }
-  if (!write) return;
-#pragma unroll
-  for (int d = 0; d < 3; ++d) {
+    return make_uint2(__byte_perm(a04, a15, 0x5410), __byte_perm(a26, a37, 0x5410));
+  };
+  auto put = [&](int d, uint2 q) {
     const int xc = m * 3 + 2 - d;  // the highest digit first
     // [t][u][8 bytes], t = l mod 4, u = l / 4
     const uint32_t off = (((l & 3) * 2 + (l >> 3)) ^ (xc & 1)) * 16 + ((l >> 2) & 1) * 8;
-    *reinterpret_cast<uint2*>(rec + xc * 128 + off) = digit[d];
-  }
-  if (l % GL == 0) {
-    float* s = reinterpret_cast<float*>(rec + R.dsum) + (l / GL) * SUMS + (PL ? m : 3 * m);
-    if constexpr (PL) {
-      const int high = (fixed + 32768) >> 16;
-      s[0] = (float)high;
-      s[V * SUMS] = (float)(fixed - high * 65536);
-    } else {
-      const int s1 = (int16_t)(upper & 0xFFFF), s2 = (upper - s1) >> 16;
-      s[0] = (float)s2;
-      s[1] = (float)s1;
-      s[2] = (float)(fixed - s2 * 65536 - s1 * 256);
+    *reinterpret_cast<uint2*>(rec + xc * 128 + off) = q;
+  };
+  float* s = reinterpret_cast<float*>(rec + R.dsum);
+  if constexpr (NT == 1) {
+    // The digits' sums over a group, of bytes (≤ 2^15, so two fit side by side in a
+    // word), before the digits are put together: with 64 registers that is 3 to 5 %
+    // of a call of long rows faster than what follows for five tokens.
+#pragma unroll
+    for (int o = 1; o < GL; o <<= 1) {
+      outer += __shfl_xor_sync(0xffffffffu, outer, o);
+      middle += __shfl_xor_sync(0xffffffffu, middle, o);
     }
+    if (!write) return;
+#pragma unroll
+    for (int d = 0; d < 3; ++d) put(d, digit(d));
+    if (l % GL == 0) {
+      constexpr int kBias = 128 * 8 * GL;
+      s += (l / GL) * SUMS + 3 * m;
+      s[0] = (float)((int)(outer >> 16) - kBias);
+      s[1] = (float)((int)middle - kBias);
+      s[2] = (float)((int)(outer & 0xFFFFu) - kBias);
+    }
+  } else {
+    int sum[3];
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+      const uint2 q = digit(d);
+      if (!PL) sum[d] = dp4a(q.y, 0x01010101u, dp4a(q.x, 0x01010101u, 0));
+      if (write) put(d, q);
+    }
+    if constexpr (PL) {  // the token's sum, |fixed| ≤ 128·2^23
+#pragma unroll
+      for (int o = 1; o < GL; o <<= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
+      if (write && l % GL == 0) {
+        s += ((l / GL) * SUMS + (m & ~1)) * 2 + (m & 1);
+        const int high = (fixed + 32768) >> 16;
+        s[0] = (float)high;
+        s[2] = (float)(fixed - high * 65536);
+      }
+    } else {
+      // The digits' sums. The first step leaves the two upper ones (≤ 2^14 each, side
+      // by side in one word) to the group's lower lanes and the lowest one to
+      // the upper lanes, so that one value per lane is left to add up.
+      const bool up = (l & (GL / 2)) != 0;
+      const int upper = sum[2] * 65536 + sum[1];
+      int v1 = (up ? sum[0] : upper) + __shfl_xor_sync(0xffffffffu, up ? upper : sum[0], GL / 2);
+#pragma unroll
+      for (int o = 1; o < GL / 2; o <<= 1) v1 += __shfl_xor_sync(0xffffffffu, v1, o);
+      if (write && l % (GL / 2) == 0) {
+        s += (l / GL) * SUMS + 3 * m;
+        if (up) {
+          s[2] = (float)v1;
+        } else {
+          const int s1 = (int16_t)(v1 & 0xFFFF);
+          s[0] = (float)((v1 - s1) >> 16);
+          s[1] = (float)s1;
+        }
+      }
+    }
+    if (!write) return;
   }
   if (l == 0) {
     float* c = reinterpret_cast<float*>(rec + R.cf) + (PL ? m : 3 * m);
@@ -308,27 +351,34 @@ __device__ __forceinline__ void w4_digits(const float (&v)[8], uint8_t* rec, con
   }
 }
 
-// Eight activations as fp32, zeros where `in` is false.
+// Eight activations as loaded, zeros where `in` is false. bf16 values stay as they
+// are until they are needed: four registers instead of eight.
 template <typename T>
-__device__ __forceinline__ void w4_load_x(const T* p, bool in, float (&v)[8]) {
+struct W4Values {
+  static constexpr int kWords = 2 * sizeof(T);
+  uint32_t a[kWords];
+  __device__ __forceinline__ void load(const T* p, bool in) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = 0.f;
-  if (!in) return;
-  if constexpr (sizeof(T) == 2) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    for (int i = 0; i < kWords; ++i) a[i] = 0u;
+    if (!in) return;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int i = 0; i < kWords; i += 4) {
+      if constexpr (sizeof(T) == 2) {  // volatile: the compiler would convert at once
+        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]) : "l"(p));
+      } else {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+        a[i] = q.x; a[i + 1] = q.y; a[i + 2] = q.z; a[i + 3] = q.w;
+      }
     }
-  } else {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 c = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = c.x; v[5] = c.y; v[6] = c.z; v[7] = c.w;
   }
-}
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = sizeof(T) == 4 ? __uint_as_float(a[j % kWords])
+                            : __uint_as_float(j & 1 ? a[j / 2] & 0xFFFF0000u : a[j / 2] << 16);
+  }
+};
 
 // A CTA's own activations into shared memory, B blocks' loads in flight
 // together.
@@ -337,7 +387,7 @@ __device__ __forceinline__ void w4_stage_x(uint8_t* x, const W4Record<V, NT>& R,
                                            int kb0, int KB, int toks) {
   const int units = KB * 16, total = units * toks;
   for (int i0 = threadIdx.x; i0 - (int)(threadIdx.x & 31) < total; i0 += B * kW4Threads) {
-    float v[B][8];
+    W4Values<T> v[B];
     int tok[B], unit_of[B];
 #pragma unroll
     for (int b = 0; b < B; ++b) {
@@ -345,13 +395,15 @@ __device__ __forceinline__ void w4_stage_x(uint8_t* x, const W4Record<V, NT>& R,
       tok[b] = toks == 1 ? 0 : i / units;
       unit_of[b] = i - tok[b] * units;
       const int64_t k = ((int64_t)kb0 * 16 + unit_of[b]) * 8;
-      w4_load_x(X + (int64_t)tok[b] * K + k, i < total && k < K, v[b]);
+      v[b].load(X + (int64_t)tok[b] * K + k, i < total && k < K);
     }
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       const int i = i0 + b * kW4Threads;
       if (i - (int)(threadIdx.x & 31) >= total) break;  // the same for the warp
-      w4_digits<V, NT>(v[b], x + (unit_of[b] >> 4) * R.bytes, R, tok[b], i < total);
+      float x8[8];
+      v[b].get(x8);
+      w4_digits<V, NT>(x8, x + (unit_of[b] >> 4) * R.bytes, R, tok[b], i < total);
     }
   }
 }
@@ -394,8 +446,10 @@ w4_digits_kernel(const T* __restrict__ X, int64_t M, int64_t K, uint8_t* __restr
   const int kb = (int)(blockIdx.x * 16 + (threadIdx.x >> 4)), l = threadIdx.x & 15;
   for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
     const int64_t k = (int64_t)kb * 128 + 8 * l;
+    W4Values<T> raw;
+    raw.load(X + m * K + k, k < K);
     float v[8];
-    w4_load_x(X + m * K + k, k < K, v);
+    raw.get(v);
     uint8_t* rec = out + ((m / TOK) * KB + kb) * (int64_t)R.bytes;
     w4_digits<V, NT>(v, rec, R, (int)(m % TOK), kb < KB);
   }
@@ -421,10 +475,10 @@ __device__ __forceinline__ uint32_t w4_centre(uint32_t w, uint32_t z) {
 // against 6.4 for 1 x 2560 -> 6912. Above five tokens, where the digits take three
 // times the MMAs and a token's sums more fp32 work than the codes, bf16
 // activations go through bf16 MMAs as they are: products are exact, a group's
-// sum is the MMA's fp32 one. 16 x 4096 -> 11008 takes 13.4 us so, 20.2 in digits.
+// sum is the MMA's fp32 one. 16 x 4096 -> 11008 takes 13.4 us so, 19.9 in digits.
 // The border at five is the head's; where a CTA has few row blocks making the
-// digits costs more than the codes: 5 x 4096 -> 4096 in groups of 32 takes 12.2 us,
-// 7.4 as bf16, and 2 x 11008 -> 4096 14.1 and 11.3.
+// digits costs more than the codes: 5 x 4096 -> 4096 in groups of 32 takes 12.1 us,
+// 7.4 as bf16, and 2 x 11008 -> 4096 12.7 and 11.3.
 //
 // Each CTA owns a slab of 16-row blocks, contiguous in memory; its 16 warps
 // take equal, contiguous runs of the slab's 1 KB blocks, so the load is even
@@ -439,9 +493,9 @@ __device__ __forceinline__ uint32_t w4_centre(uint32_t w, uint32_t z) {
 // and one for the weights are what is left; 3 x 2048 -> 128256 32 us, 4.3 TB/s, 67 %
 // of the copy rate, the issue slots 64 % full; 16 x 4096 -> 11008 with zero points
 // and groups of 64 13.4 us from bf16, no unit above 45 %: the one CTA of an SM
-// waits for all its activations before the first MMA (20.2 us from fp32 with the
+// waits for all its activations before the first MMA (19.9 us from fp32 with the
 // launch that makes the digits, 24 MMAs per 1 KB block).
-template <typename T, int V, int NT>
+template <typename T, int V, int NT, int D>
 __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Params p) {
   using C = W4Pass<NT>;
   constexpr int SUMS = C::kSums, TOK = C::kTok, ST = w4_stage_bytes<V>();
@@ -449,7 +503,6 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
   extern __shared__ __align__(128) uint8_t w4_mem[];
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  constexpr int D = w4_stages<V, NT>();
   const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
   // Blocks are counted in 32 bits: 2^31 of them are 2 TB.
   const int KBt = (int)((p.K + 127) / 128);
@@ -462,7 +515,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
   const int64_t m0 = (int64_t)blockIdx.y * TOK;
   const int toks = (int)min((int64_t)TOK, p.M - m0);
   const W4Smem L = w4_smem<V, NT>((KBt + ranks - 1) / ranks, p.slab_rows + (p.slab_more > 0 ? 1 : 0),
-                                  (int)min((int64_t)TOK, p.M), ranks);
+                                  (int)min((int64_t)TOK, p.M), ranks, D);
   float* part = reinterpret_cast<float*>(w4_mem + L.part);
   float* out = reinterpret_cast<float*>(w4_mem + L.out);
 
@@ -535,8 +588,9 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
     xaddr[n] = smem_u32(x) + xc * 128 + 16 * ((2 * t) ^ (xc & 1));
     xother[n] = xaddr[n] ^ 16u;
   }
-  uint32_t sums = smem_u32(x) + R.dsum + 8 * t;
-  constexpr uint32_t CF = (C::kPlanar ? 2 : 1) * V * SUMS * 4;  // from the sums to what they count
+  uint32_t sums = smem_u32(x) + R.dsum + (C::kPlanar ? 16 : 8) * t;
+  // From the sums to what they count.
+  const uint32_t CF = C::kPlanar ? 2 * V * SUMS * 4 - 8 * t : V * SUMS * 4;
   const bool zs = p.zeros != nullptr;
   // The bits of 1.5·2^23 in four registers, out of the compiler's sight: it would
   // set them anew for every group.
@@ -649,29 +703,32 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 2 : 1) w4_linear_kernel(
           const float c0 = __uint_as_float(cq.x), c1 = __uint_as_float(cq.y);
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            const uint2 dq = lds64(sums + (v * SUMS + 8 * n) * 4);
-            const float t[4] = {__uint_as_float(dq.x), __uint_as_float(dq.y), __uint_as_float(dq.x),
-                                __uint_as_float(dq.y)};
             // Less z times the activations' sum, within the group and its digit: an
             // exact integer below 2^19. What is scaled and added up is then
-            // Σ (q − z)·d, and nothing of the size of z·Σ|x| is ever rounded.
+            // Σ (q − z)·d, and nothing of the size of z·Σ|x| is ever rounded. Three
+            // tiles: the highest digit is less z times the sum's multiple of
+            // 2^16, the two others join it, each sum exact below 2^24, and the sum's
+            // rest goes last: off by 2^-24 of the group's result, or by nothing.
+            float t0, t1, r0 = 0.f, r1 = 0.f;
+            if constexpr (C::kPlanar) {
+              const uint4 q = lds128(sums + (2 * v * SUMS + 16 * n) * 4);
+              t0 = __uint_as_float(q.x);
+              t1 = __uint_as_float(q.y);
+              r0 = __uint_as_float(q.z);
+              r1 = __uint_as_float(q.w);
+            } else {
+              const uint2 q = lds64(sums + (v * SUMS + 8 * n) * 4);
+              t0 = __uint_as_float(q.x);
+              t1 = __uint_as_float(q.y);
+            }
             float y[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              y[e] = fmaf(e < 2 ? z0[v] : z1[v], t[e], __int_as_float(d[0][v][e]) - 12582912.0f);
-            if constexpr (C::kPlanar) {
-              // The highest digit is less z times the sum's multiple of 2^16. The two
-              // others join it, each sum exact below 2^24, and the sum's rest goes
-              // last: off by 2^-24 of the group's result, or by nothing.
-              const uint2 rq = lds64(sums + ((V + v) * SUMS + 8 * n) * 4);
-              const float r[4] = {__uint_as_float(rq.x), __uint_as_float(rq.y), __uint_as_float(rq.x),
-                                  __uint_as_float(rq.y)};
+            for (int e = 0; e < 4; ++e) {
+              const float z = e < 2 ? z0[v] : z1[v];
+              y[e] = fmaf(z, e & 1 ? t1 : t0, __int_as_float(d[0][v][e]) - 12582912.0f);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                for (int j = 1; j < ND; ++j) y[e] = fmaf(y[e], 256.0f, __int_as_float(d[j][v][e]) - 12582912.0f);
-                y[e] = fmaf(e < 2 ? z0[v] : z1[v], r[e], y[e]);
-              }
+              for (int j = 1; j < ND; ++j) y[e] = fmaf(y[e], 256.0f, __int_as_float(d[j][v][e]) - 12582912.0f);
+              if constexpr (C::kPlanar) y[e] = fmaf(z, e & 1 ? r1 : r0, y[e]);
             }
             acc[n][0] = fmaf(y[0], s0[v] * c0, acc[n][0]);
             acc[n][1] = fmaf(y[1], s0[v] * c1, acc[n][1]);
