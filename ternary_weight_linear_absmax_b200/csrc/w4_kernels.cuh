@@ -488,7 +488,7 @@ __device__ __forceinline__ uint32_t w4_centre(uint32_t w, uint32_t z) {
 // cluster share a slab: each takes a range of K, so that its activations fit
 // in shared memory, and the slab's sums meet there, in the order of the CTAs.
 //
-// Measured (one B200, calls in a graph): 1 x 2560 -> 6912 6.4 us and
+// Measured (one B200, calls in a graph): 1 x 2560 -> 6912 6.5 us and
 // 4 x 512 -> 256 5.5 us, where a dependent launch, one trip for the activations
 // and one for the weights are what is left; 3 x 2048 -> 128256 32 us, 4.3 TB/s, 67 %
 // of the copy rate, the issue slots 64 % full; 16 x 4096 -> 11008 with zero points
